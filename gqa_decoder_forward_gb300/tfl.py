@@ -32,6 +32,7 @@ TFL_E_DEVICE = -8
 TFL_KV_PAGE = 128
 
 _vp = ctypes.c_void_p
+_intp = ctypes.POINTER(ctypes.c_int)
 
 
 class tfl_config(ctypes.Structure):
@@ -105,6 +106,21 @@ SIGNATURES = {
     "tfl_profile_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_long)]),
     "tfl_profile_kind": (ctypes.c_char_p, [ctypes.c_int]),
+    "tfl_kv4_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "tfl_kv4_alloc": (ctypes.c_int, [ctypes.c_int] * 4 + [_vp, ctypes.c_size_t, ctypes.POINTER(_vp)]),
+    "tfl_kv4_free": (None, [_vp]),
+    "tfl_kv4_reset": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "tfl_kv4_length": (ctypes.c_int, [_vp]),
+    "tfl_kv4_capacity": (ctypes.c_int, [_vp]),
+    "tfl_kv4_write": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]),
+    "tfl_kv4_read": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp, _vp,
+                                    ctypes.c_size_t, _vp]),
+    "tfl_kv4_attn_bytes": (ctypes.c_size_t, [ctypes.c_int] * 5),
+    "tfl_kv4_attn_init": (ctypes.c_int, [ctypes.c_int] * 5 + [_vp, ctypes.c_size_t, ctypes.POINTER(_vp)]),
+    "tfl_kv4_attn_free": (None, [_vp]),
+    "tfl_kv4_attention": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp,
+                                         ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -457,3 +473,123 @@ def tfl_profile_read(model: Model) -> dict:
     cnt = (ctypes.c_long * len(names))()
     _check(lib().tfl_profile_read(model.handle, len(names), ms, cnt))
     return {names[i]: (ms[i], cnt[i]) for i in range(len(names))}
+
+
+# ---- 4-bit KV cache -----------------------------------------------------------------
+
+def tfl_kv4_bytes(layers: int, n_kv: int, max_positions: int, head_dim: int = 128) -> int:
+    return int(lib().tfl_kv4_bytes(layers, n_kv, head_dim, max_positions))
+
+
+class KV4:
+    """A paged cache in 4 bits (tfl_kv4) over `buffer` (a uint8 CUDA tensor of at
+    least tfl_kv4_bytes bytes, whose contents are kept) or one that it allocates."""
+
+    def __init__(self, layers: int, n_kv: int, max_positions: int, buffer: torch.Tensor = None):
+        nbytes = tfl_kv4_bytes(layers, n_kv, max_positions)
+        if buffer is None:
+            buffer = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        self.layers, self.n_kv, self.buffer = layers, n_kv, buffer
+        h = _vp()
+        _check(lib().tfl_kv4_alloc(layers, n_kv, 128, int(max_positions), _ptr(buffer),
+                                   buffer.numel() * buffer.element_size(), ctypes.byref(h)))
+        self.handle = h
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            lib().tfl_kv4_free(self.handle)
+            self.handle = None
+
+    @property
+    def length(self) -> int:
+        return int(lib().tfl_kv4_length(self.handle))
+
+    @property
+    def capacity(self) -> int:
+        return int(lib().tfl_kv4_capacity(self.handle))
+
+    def reset(self, keep: int):
+        _check(lib().tfl_kv4_reset(self.handle, int(keep)))
+
+
+class KV4Rows:
+    """Rows of a call over 4-bit caches: stream s has rows[s] rows at positions
+    pos0[s] on.  Keeps the host arrays that the library takes, so that a step's
+    layers (and, with set, its successors) make them once."""
+
+    def __init__(self, kvs: Sequence[KV4], pos0: Sequence[int], rows: Sequence[int]):
+        self.kvs = list(kvs)
+        self.n = len(self.kvs)
+        self.handles = (_vp * self.n)(*[kv.handle for kv in self.kvs])
+        self.pos0 = (ctypes.c_int * self.n)()
+        self.rows = (ctypes.c_int * self.n)()
+        self.set(pos0, rows)
+
+    def set(self, pos0: Sequence[int], rows: Sequence[int]):
+        if len(pos0) != self.n or len(rows) != self.n:
+            raise ValueError(f"{len(pos0)} positions and {len(rows)} row counts for {self.n} caches")
+        self.pos0[:] = pos0
+        self.rows[:] = rows
+        self.total = sum(rows)
+        self.n_kv = self.kvs[0].n_kv if self.kvs else 0
+
+
+class KV4Attention:
+    """tfl_kv4_attn and its workspace: attention of up to max_rows rows over caches
+    of up to max_positions positions."""
+
+    def __init__(self, n_q: int, n_kv: int, max_rows: int = 16, max_positions: int = 4096):
+        nbytes = int(lib().tfl_kv4_attn_bytes(n_q, n_kv, 128, max_rows, max_positions))
+        self.n_q, self.n_kv = n_q, n_kv
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device="cuda")
+        h = _vp()
+        _check(lib().tfl_kv4_attn_init(n_q, n_kv, 128, max_rows, max_positions, _ptr(self.workspace), nbytes,
+                                       ctypes.byref(h)))
+        self.handle = h
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            lib().tfl_kv4_attn_free(self.handle)
+            self.handle = None
+
+
+def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:
+    """Row stride (elements) of a bf16 CUDA tensor of at least n rows of heads x 128
+    numbers, [rows, heads, 128] or [rows, heads * 128]; only rows may be strided."""
+    sh, st = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError("expected a bf16 CUDA tensor")
+    if len(sh) == 2:
+        ok = sh[1] == heads * 128 and st[1] == 1
+    else:
+        ok = len(sh) == 3 and sh[1] == heads and sh[2] == 128 and st[2] == 1 and (heads == 1 or st[1] == 128)
+    if not ok or sh[0] < n:
+        raise ValueError(f"expected [>= {n}, {heads} * 128] with contiguous rows, got {tuple(sh)} strides {st}")
+    return st[0] if sh[0] > 1 else heads * 128
+
+
+def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """Quantises rows k, v into the caches of batch."""
+    ld = _rows_arg(k, batch.total, batch.n_kv)
+    if _rows_arg(v, batch.total, batch.n_kv) != ld:
+        raise ValueError("k and v have different row strides")
+    return _check(lib().tfl_kv4_write(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
+                                      v.data_ptr(), ld, _stream(stream)))
+
+
+def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """Reads what the caches of batch stand for into k, v."""
+    ld = _rows_arg(k, batch.total, batch.n_kv)
+    if _rows_arg(v, batch.total, batch.n_kv) != ld:
+        raise ValueError("k and v have different row strides")
+    return _check(lib().tfl_kv4_read(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
+                                     v.data_ptr(), ld, _stream(stream)))
+
+
+def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.Tensor, out: torch.Tensor,
+                      stream=None):
+    """Attention of the rows q over the caches of batch (which hold those rows' own keys and values)."""
+    ldq = _rows_arg(q, batch.total, attn.n_q)
+    ldo = _rows_arg(out, batch.total, attn.n_q)
+    return _check(lib().tfl_kv4_attention(attn.handle, batch.handles, batch.n, layer, batch.pos0, batch.rows,
+                                          q.data_ptr(), ldq, out.data_ptr(), ldo, _stream(stream)))

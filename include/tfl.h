@@ -459,6 +459,102 @@ int tfl_layer_op(tfl_model* model, int op, int layer, tfl_kv* kv, int pos0, int 
 int tfl_attention_decode_noalloc(tfl_kv* kv, int layer, int pos0, int rows, const void* q, void* out,
                                  void* stream);
 
+/* ---- 4-bit KV cache ------------------------------------------------------------ */
+
+/*
+ * A paged cache that holds keys (after RoPE) and values in 4 bits, for contexts
+ * and stream counts whose bf16 cache would not fit or would bound the step:
+ * 144 bytes a position and KV head (64 of key codes, 64 of value codes, 16 of
+ * scales and zeros) against 512.  The pages serve a bf16 cache and have no
+ * counterpart.
+ *
+ * What is held.  Per position and head, keys and values each in two groups of 64
+ * dims (0..63, 64..127).  A group of bf16 numbers x is held as
+ *   zero = min x,  scale = bf16((max x - min x) / 15),
+ *   n = clamp(round((x - zero) / scale), 0, 15) (nearest, ties to even; 0 when scale = 0)
+ * computed in fp32, and stands for zero + scale * n: at most half a scale from x,
+ * plus the rounding of the scale (relative 2^-9, at most 15 * 2^-9 of a scale).
+ * A group with a NaN or an infinity, or whose max - min overflows fp32, stands
+ * for NaN in all its dims.
+ *
+ * Layout of a buffer: the page table (int32 per page of TFL_KV_PAGE positions,
+ * padded to 256 bytes, identity after tfl_kv4_alloc), then one tile of
+ * TFL_KV4_TILE bytes per (layer, page, KV head):
+ *   tile(layer, pos, head) at tiles + ((layer*n_pages + table[pos/PAGE])*n_kv + head) * TFL_KV4_TILE
+ * A tile is eight blocks of 16 positions, a block 2,304 bytes: 16 rows of key
+ * codes (64 bytes each), 16 x (scale, zero of group 0, scale, zero of group 1) of
+ * the keys (bf16), then the same two parts for the values.  In a row, dims
+ * 8c..8c+7 are the first and 64+8c..64+8c+7 the second 32-bit word of 8-byte chunk
+ * c, the lowest dim in the lowest 4 bits; chunk c is stored as chunk c ^ 4 at
+ * positions whose bit 1 is set.
+ *
+ * Independent of any model: layers 1..1024, n_kv 1..64 heads, head_dim 128, max_positions
+ * 1..2^20.  bytes: 0 for sizes outside these.  tfl_kv4_alloc: dev_buf 16-byte
+ * aligned device memory of the current device, owned by the caller and kept
+ * alive; writes the page table (synchronously) and nothing else, so a buffer
+ * filled before keeps its contents; the length starts at 0.  reset, length and
+ * capacity as tfl_kv_reset, tfl_kv_length and tfl_kv_capacity.
+ */
+#define TFL_KV4_GROUP 64
+#define TFL_KV4_TILE 18432
+typedef struct tfl_kv4 tfl_kv4;
+size_t tfl_kv4_bytes(int layers, int n_kv, int head_dim, int max_positions);
+int tfl_kv4_alloc(int layers, int n_kv, int head_dim, int max_positions, void* dev_buf, size_t bytes, tfl_kv4** out);
+void tfl_kv4_free(tfl_kv4* kv);
+int tfl_kv4_reset(tfl_kv4* kv, int keep);
+int tfl_kv4_length(const tfl_kv4* kv);
+int tfl_kv4_capacity(const tfl_kv4* kv);
+
+/*
+ * Quantises rows into the cache, and reads back what the cache stands for.
+ * n_streams (1..16) caches of the same n_kv; stream s has rows[s] >= 0 rows (host
+ * array; 0: the stream sits this call out) at positions pos0[s] .. pos0[s] + rows[s] - 1
+ * (host array), which must lie inside its capacity; its rows follow those of the
+ * streams before it.  k, v: device bf16, row r of head h at k + r*ld + 128*h
+ * elements, so they may be parts of wider rows; ld >= 128 n_kv and a multiple of 8,
+ * k and v 16-byte aligned.  Rows of k and v past the last stream's are neither read
+ * nor written.  write: k, v -> cache, which must not name one cache twice; read:
+ * cache -> k, v, each number rounded once more to bf16; k and v must not overlap.
+ * Neither changes a length.  Both enqueue one kernel on stream and allocate
+ * nothing (they may be captured into a graph).  The current device must be the
+ * caches' device.
+ */
+int tfl_kv4_write(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0, const int* rows, const void* k,
+                  const void* v, size_t ld, void* stream);
+int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0, const int* rows, void* k, void* v,
+                 size_t ld, void* stream);
+
+/*
+ * Attention over 4-bit caches: row i of stream s (rows[s] in 0..16, at most
+ * max_rows rows in all) sits at position pos0[s] + i and attends keys 0 .. pos0[s] + i
+ * of its cache, which must hold them (its own row's too): scale 1/sqrt(128), softmax
+ * and sums in fp32 over the numbers that the codes stand for (not rounded to
+ * bf16), the output rounded once.  Query head j reads KV head j / (n_q / n_kv).
+ * q, out: device bf16, row r of head j at q + r*ldq + 128*j (out + r*ldo + 128*j);
+ * ldq, ldo >= 128 n_q and multiples of 8; both 16-byte aligned, not overlapping.
+ * Rows past the last stream's are left as they were.  A cache may be named more
+ * than once (several rows of a shared prompt).  A key or value that stands for NaN
+ * makes the heads that attend it NaN; positions a row does not attend never
+ * matter, whatever their bytes.
+ * A row's result depends on its own query and its cache alone, bit for bit: not
+ * on the other rows, streams or the capacity.
+ *
+ * tfl_kv4_attn holds the sizes and the caller's device workspace (256-byte
+ * aligned, tfl_kv4_attn_bytes bytes, used by this object alone until it is freed):
+ * n_kv 1..64, n_q = n_kv times 1..16, head_dim 128, max_rows 1..64, max_positions
+ * 1..2^20 (the largest pos0 + rows).  Calls of one object must not overlap on
+ * the GPU (one stream, or events; two graphs captured with one object must not run
+ * at once); calls with different objects may.  A call allocates nothing and may be
+ * captured.
+ */
+typedef struct tfl_kv4_attn tfl_kv4_attn;
+size_t tfl_kv4_attn_bytes(int n_q, int n_kv, int head_dim, int max_rows, int max_positions);
+int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_positions, void* workspace,
+                      size_t ws_bytes, tfl_kv4_attn** out);
+void tfl_kv4_attn_free(tfl_kv4_attn* attn);
+int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
+                      const int* rows, const void* q, size_t ldq, void* out, size_t ldo, void* stream);
+
 /* ---- per-kernel timing ------------------------------------------------------------- */
 
 /*
