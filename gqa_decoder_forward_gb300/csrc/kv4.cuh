@@ -102,14 +102,18 @@ struct AttnArgs {
     long ldq;
     bf16* out;
     long ldo;
-    float* pm;           // [row][q head][max_units]
-    float* pl;
-    float* po;           // [row][q head][max_units][128]
-    int max_units;
+    float *pm, *pl;      // a unit's maximum and sum: [row][q head][max_units]
+    float* po;           // and output: [row][q head][max_units][128]
+    float *gm, *gl, *go; // the same of a group of units: [row][q head][max_groups]
+    unsigned* counters;  // [(stream, columns, head)][max_counters]: arrivals of groups, then of each group's units; 0 between calls
+    int max_units, max_groups, max_counters;
+    int item_start[kMaxStreams + 1];  // set by launch_attn: first CTA of a stream,
+    int set_start[kMaxStreams];       // and its first set of columns
 };
 int attn_unit();         // keys of one partial
+int attn_fan();          // partials joined at a time
 cudaError_t init_attn();
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_attn(AttnArgs& a, cudaStream_t st, bool pdl);
 
 }  // namespace kv4
 }  // namespace tfl
@@ -125,6 +129,7 @@ struct tfl_kv4 {
 
 struct tfl_kv4_attn {
     int device;
-    int n_q, n_kv, max_rows, max_pos, max_units;
-    float *pm, *pl, *po;
+    int n_q, n_kv, max_rows, max_pos, max_units, max_groups;
+    float *pm, *pl, *po, *gm, *gl, *go;
+    unsigned* counters;
 };

@@ -60,6 +60,36 @@ bool attn_sizes_ok(int n_q, int n_kv, int head_dim, int max_rows, int max_positi
            max_positions >= 1 && max_positions <= kMaxPositions;
 }
 
+// Workspace of an attention object (byte offsets, 256-byte aligned regions).
+struct AttnLayout {
+    size_t pm, pl, po, gm, gl, go, counters, total;
+    int units, groups;
+};
+
+AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
+    AttnLayout L;
+    L.units = (max_positions + kv4::attn_unit() - 1) / kv4::attn_unit();
+    L.groups = (L.units + kv4::attn_fan() - 1) / kv4::attn_fan();
+    const size_t cols = (size_t)max_rows * n_q;
+    // sets of eight columns or more of one stream and KV head: at most these, however the rows are spread
+    const size_t sets = (size_t)max_rows * ((n_q / n_kv + 7) / 8) * n_kv;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = round256(off + bytes);
+        return o;
+    };
+    L.pm = take(cols * L.units * 4);
+    L.pl = take(cols * L.units * 4);
+    L.po = take(cols * L.units * kHeadDim * 4);
+    L.gm = take(cols * L.groups * 4);
+    L.gl = take(cols * L.groups * 4);
+    L.go = take(cols * L.groups * kHeadDim * 4);
+    L.counters = take(sets * (1 + L.groups) * 4);
+    L.total = off;
+    return L;
+}
+
 // The current device, if it is one this library runs on.
 int check_arch(int* dev) {
     CK(cudaGetDevice(dev));
@@ -212,9 +242,7 @@ int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
 
 size_t tfl_kv4_attn_bytes(int n_q, int n_kv, int head_dim, int max_rows, int max_positions) {
     if (!attn_sizes_ok(n_q, n_kv, head_dim, max_rows, max_positions)) return 0;
-    const size_t units = (size_t)(max_positions + kv4::attn_unit() - 1) / kv4::attn_unit();
-    const size_t parts = (size_t)max_rows * n_q * units;
-    return 2 * round256(parts * 4) + parts * kHeadDim * 4;
+    return attn_layout(n_q, n_kv, max_rows, max_positions).total;
 }
 
 int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_positions, void* workspace,
@@ -240,11 +268,23 @@ int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_pos
     a->n_kv = n_kv;
     a->max_rows = max_rows;
     a->max_pos = max_positions;
-    a->max_units = (max_positions + kv4::attn_unit() - 1) / kv4::attn_unit();
-    const size_t parts = (size_t)max_rows * n_q * a->max_units;
-    a->pm = (float*)workspace;
-    a->pl = (float*)((char*)workspace + round256(parts * 4));
-    a->po = (float*)((char*)workspace + 2 * round256(parts * 4));
+    const AttnLayout L = attn_layout(n_q, n_kv, max_rows, max_positions);
+    char* ws = (char*)workspace;
+    a->max_units = L.units;
+    a->max_groups = L.groups;
+    a->pm = (float*)(ws + L.pm);
+    a->pl = (float*)(ws + L.pl);
+    a->po = (float*)(ws + L.po);
+    a->gm = (float*)(ws + L.gm);
+    a->gl = (float*)(ws + L.gl);
+    a->go = (float*)(ws + L.go);
+    a->counters = (unsigned*)(ws + L.counters);
+    // the counters start at zero; every call leaves them zero again
+    const cudaError_t ce = cudaMemset(a->counters, 0, L.total - L.counters);
+    if (ce != cudaSuccess) {
+        delete a;
+        return fail(TFL_E_CUDA, "clearing the workspace's counters failed: %s", cudaGetErrorString(ce));
+    }
     *out = a;
     return ok();
 }
@@ -277,7 +317,13 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
     a.pm = attn->pm;
     a.pl = attn->pl;
     a.po = attn->po;
+    a.gm = attn->gm;
+    a.gl = attn->gl;
+    a.go = attn->go;
+    a.counters = attn->counters;
     a.max_units = attn->max_units;
+    a.max_groups = attn->max_groups;
+    a.max_counters = 1 + attn->max_groups;
     CK(kv4::launch_attn(a, (cudaStream_t)stream, false));
     return ok();
 }

@@ -425,3 +425,55 @@ def test_calls_that_are_refused_change_nothing():
     at(attn, rows([kv, kv], [0, 9], [0, 0]), 0, q, out)
     torch.cuda.synchronize()
     same_bytes(host, kv)
+
+
+# ---- long caches: partials joined in groups -------------------------------------------------
+
+@pytest.mark.parametrize("pos0", [8186, 16378, 511 - 6])
+def test_windows_across_a_group_of_units_equal_single_rows_call_after_call(pos0):
+    """512 keys a unit, 16 units a group: rows on both sides of the border, several calls of one object."""
+    rows = 12
+    kv, kq, vq = filled(140, 2, pos0 + rows, pos0 + rows)
+    q = queries(141, rows, 14)
+    attn = tfl.KV4Attention(14, 2, max_rows=16, max_positions=pos0 + 1000)
+    window = attend(attn, [kv], [pos0], [rows], q)
+    for i in range(rows):
+        assert (attend(attn, [kv], [pos0 + i], [1], q[i: i + 1])[0] == window[i]).all()
+    assert (attend(attn, [kv], [pos0], [rows], q) == window).all()
+    check(window[::11], q[::11], [pos0, pos0 + 11], kq, vq)
+
+
+def test_the_longest_capacity_and_positions_past_2_gib():
+    """Positions whose byte offsets pass 32 bits: 64 heads, the last layer's tile of a 300,000-position cache."""
+    n_kv, cap, layers = 64, 300000, 2
+    kv = tfl.KV4(layers, n_kv, cap)
+    assert kv.buffer.numel() > 2 ** 32
+    pos0, n = cap - 20, 20
+    k, v = rows_like_keys(150, n, n_kv), rows_like_keys(151, n, n_kv)
+    b = tfl.KV4Rows([kv], [pos0], [n])
+    tfl.tfl_kv4_write(b, 1, cuda_bf16(k), cuda_bf16(v))
+    gk = torch.empty((n, n_kv, 128), dtype=torch.bfloat16, device="cuda")
+    gv = torch.empty_like(gk)
+    tfl.tfl_kv4_read(b, 1, gk, gv)
+    for got, x in ((gk, k), (gv, v)):
+        w = ref.values(*ref.quantise(x))
+        assert (np.abs(host_f32(got) - w) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(w)).all()
+    # the same last keys under every earlier position zero: all earlier keys score 0 and stand for 0
+    kv.buffer[((cap + 127) // 128 * 4 + 255) // 256 * 256:].zero_()
+    tfl.tfl_kv4_write(b, 1, cuda_bf16(k), cuda_bf16(v))
+    attn = tfl.KV4Attention(n_kv, n_kv, max_rows=1, max_positions=cap)
+    q = queries(152, 1, n_kv)
+    got = attend(attn, [kv], [cap - 1], [1], q, layer=1)
+    kq, vq = values64(k), values64(v)
+    for h in range(n_kv):
+        s = np.concatenate([np.zeros(pos0), kq[:, h] @ q[0, h].astype(np.float64) / np.sqrt(128)])
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        want = p[pos0:] @ vq[:, h]
+        # the reference's bound with V zero before pos0: 2^-8 and 2^-7 of sum P |V|'s terms (|z| + s n <= 3 max |x| here)
+        tol = 2.0 ** -7 * np.abs(want) + 2.0 ** -10 * (p[pos0:] @ (3 * np.abs(v[:, h]).max() * np.ones((n, 128))))
+        assert (np.abs(got[0, h] - want) <= tol).all()
+
+
+def values64(x):
+    return ref.values(*ref.quantise(x))
