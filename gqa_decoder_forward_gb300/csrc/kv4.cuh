@@ -102,10 +102,12 @@ struct AttnArgs {
     long ldq;
     bf16* out;
     long ldo;
-    float *pm, *pl;      // a unit's maximum and sum: [row][q head][max_units]
-    float* po;           // and output: [row][q head][max_units][128]
-    float *gm, *gl, *go; // the same of a group of units: [row][q head][max_groups]
-    unsigned* counters;  // [(stream, columns, head)][max_counters]: arrivals of groups, then of each group's units; 0 between calls
+    // partials of (stream, columns, KV head) "sets": per unit, and per group of units,
+    // the maxima and sums [set][unit][column of the set's tiles] and the outputs
+    // [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
+    float *pm, *pl, *po;
+    float *gm, *gl, *go;
+    unsigned* counters;  // [set][max_counters]: arrivals of groups, then of each group's units; 0 between calls
     int max_units, max_groups, max_counters;
     int item_start[kMaxStreams + 1];  // set by launch_attn: first CTA of a stream,
     int set_start[kMaxStreams];       // and its first set of columns

@@ -1,5 +1,6 @@
 // C entry points of the 4-bit cache (include/tfl.h): argument checks, sizes and
 // enqueueing.  The kernels are in kv4_cache.cu and kv4_attn.cu.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -70,22 +71,23 @@ AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
     AttnLayout L;
     L.units = (max_positions + kv4::attn_unit() - 1) / kv4::attn_unit();
     L.groups = (L.units + kv4::attn_fan() - 1) / kv4::attn_fan();
-    const size_t cols = (size_t)max_rows * n_q;
-    // sets of eight columns or more of one stream and KV head: at most these, however the rows are spread
-    const size_t sets = (size_t)max_rows * ((n_q / n_kv + 7) / 8) * n_kv;
+    // Tiles of eight columns over all sets.  A call has at most 16 streams; one of R rows has
+    // ceil(R G / 8) tiles per KV head if every stream has one, else 2 ceil(R G / 16).
+    const int G = n_q / n_kv;
+    const size_t tiles = (size_t)n_kv * 2 * (std::min(max_rows, kMaxStreams) + (max_rows * G + 15) / 16);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t o = off;
         off = round256(off + bytes);
         return o;
     };
-    L.pm = take(cols * L.units * 4);
-    L.pl = take(cols * L.units * 4);
-    L.po = take(cols * L.units * kHeadDim * 4);
-    L.gm = take(cols * L.groups * 4);
-    L.gl = take(cols * L.groups * 4);
-    L.go = take(cols * L.groups * kHeadDim * 4);
-    L.counters = take(sets * (1 + L.groups) * 4);
+    L.pm = take(tiles * L.units * 8 * 4);
+    L.pl = take(tiles * L.units * 8 * 4);
+    L.po = take(tiles * L.units * 8 * kHeadDim * 4);
+    L.gm = take(tiles * L.groups * 8 * 4);
+    L.gl = take(tiles * L.groups * 8 * 4);
+    L.go = take(tiles * L.groups * 8 * kHeadDim * 4);
+    L.counters = take(tiles * (1 + L.groups) * 4);  // a set has at least one tile
     L.total = off;
     return L;
 }

@@ -477,3 +477,24 @@ def test_the_longest_capacity_and_positions_past_2_gib():
 
 def values64(x):
     return ref.values(*ref.quantise(x))
+
+
+def test_many_units_on_single_warps_equal_few_units_on_whole_ctas():
+    """A call of many (unit, KV head) pairs gives each unit to a warp, one of few gives each element of a unit to a warp, and
+    wide windows take two tiles of columns: the same bits."""
+    n_kv, pos0, rows = 64, 8300, 9
+    kv, kq, vq = filled(160, n_kv, pos0 + rows, pos0 + rows)
+    q = queries(161, rows, n_kv)
+    attn = tfl.KV4Attention(n_kv, n_kv, max_rows=16, max_positions=pos0 + rows)
+    window = attend(attn, [kv], [pos0], [rows], q)                     # two tiles
+    one = attend(attn, [kv], [pos0], [8], q[:8])                       # one tile, 17 units x 64 heads
+    several = attend(attn, [kv] * 9, [pos0 + i for i in range(9)], [1] * 9, q)
+    assert (one == window[:8]).all() and (several == window).all()
+    check(window[:1], q[:1], [pos0], kq, vq)
+    kv8, _, _ = filled(162, 8, 70000, 70000)                           # 137 units x 8 heads
+    q8 = queries(163, 2, 56)
+    few = tfl.KV4Attention(56, 8, max_rows=16, max_positions=70000)
+    for p in (69999, 66047, 66048, 65600):
+        w = attend(few, [kv8], [p - 1], [2], q8)                       # two tiles
+        for i in range(2):
+            assert (attend(few, [kv8], [p - 1 + i], [1], q8[i: i + 1])[0] == w[i]).all()
