@@ -102,20 +102,16 @@ struct AttnArgs {
     long ldq;
     bf16* out;
     long ldo;
-    // partials of (stream, columns, KV head) "sets": per unit, and per group of units,
-    // the maxima and sums [set][unit][column of the set's tiles] and the outputs
-    // [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
+    // partials of (stream, columns, KV head) "sets", per unit: maxima and sums
+    // [set][unit][column of the set's tiles], outputs [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
     float *pm, *pl, *po;
-    float *gm, *gl, *go;
-    unsigned* counters;  // [set][max_counters]: arrivals of groups, then of each group's units; 0 between calls
-    int max_units, max_groups, max_counters;
-    int item_start[kMaxStreams + 1];  // set by launch_attn: first CTA of a stream,
+    int max_units;
+    int item_start[kMaxStreams + 1];  // set by launch_attn: first unit (over its sets) of a stream,
     int set_start[kMaxStreams];       // and its first set of columns
 };
 int attn_unit();         // keys of one partial
-int attn_fan();          // partials joined at a time
 cudaError_t init_attn();
-cudaError_t launch_attn(AttnArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl);
 
 }  // namespace kv4
 }  // namespace tfl
@@ -131,7 +127,7 @@ struct tfl_kv4 {
 
 struct tfl_kv4_attn {
     int device;
-    int n_q, n_kv, max_rows, max_pos, max_units, max_groups;
-    float *pm, *pl, *po, *gm, *gl, *go;
-    unsigned* counters;
+    int n_q, n_kv, max_rows, max_pos, max_units;
+    int sms;  // of the device
+    float *pm, *pl, *po;
 };

@@ -63,14 +63,13 @@ bool attn_sizes_ok(int n_q, int n_kv, int head_dim, int max_rows, int max_positi
 
 // Workspace of an attention object (byte offsets, 256-byte aligned regions).
 struct AttnLayout {
-    size_t pm, pl, po, gm, gl, go, counters, total;
-    int units, groups;
+    size_t pm, pl, po, total;
+    int units;
 };
 
 AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
     AttnLayout L;
     L.units = (max_positions + kv4::attn_unit() - 1) / kv4::attn_unit();
-    L.groups = (L.units + kv4::attn_fan() - 1) / kv4::attn_fan();
     // Tiles of eight columns over all sets.  A call has at most 16 streams; one of R rows has
     // ceil(R G / 8) tiles per KV head if every stream has one, else 2 ceil(R G / 16).
     const int G = n_q / n_kv;
@@ -84,10 +83,6 @@ AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
     L.pm = take(tiles * L.units * 8 * 4);
     L.pl = take(tiles * L.units * 8 * 4);
     L.po = take(tiles * L.units * 8 * kHeadDim * 4);
-    L.gm = take(tiles * L.groups * 8 * 4);
-    L.gl = take(tiles * L.groups * 8 * 4);
-    L.go = take(tiles * L.groups * 8 * kHeadDim * 4);
-    L.counters = take(tiles * (1 + L.groups) * 4);  // a set has at least one tile
     L.total = off;
     return L;
 }
@@ -262,6 +257,8 @@ int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_pos
     if (ws_bytes < need) return fail(TFL_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     int dev = 0;
     if (int e = check_arch(&dev)) return e;
+    int sms = 0;
+    CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     CK(kv4::init_attn());
     tfl_kv4_attn* a = new (std::nothrow) tfl_kv4_attn();
     if (!a) return fail(TFL_E_ARG, "out of host memory");
@@ -273,20 +270,10 @@ int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_pos
     const AttnLayout L = attn_layout(n_q, n_kv, max_rows, max_positions);
     char* ws = (char*)workspace;
     a->max_units = L.units;
-    a->max_groups = L.groups;
     a->pm = (float*)(ws + L.pm);
     a->pl = (float*)(ws + L.pl);
     a->po = (float*)(ws + L.po);
-    a->gm = (float*)(ws + L.gm);
-    a->gl = (float*)(ws + L.gl);
-    a->go = (float*)(ws + L.go);
-    a->counters = (unsigned*)(ws + L.counters);
-    // the counters start at zero; every call leaves them zero again
-    const cudaError_t ce = cudaMemset(a->counters, 0, L.total - L.counters);
-    if (ce != cudaSuccess) {
-        delete a;
-        return fail(TFL_E_CUDA, "clearing the workspace's counters failed: %s", cudaGetErrorString(ce));
-    }
+    a->sms = sms;
     *out = a;
     return ok();
 }
@@ -319,14 +306,8 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
     a.pm = attn->pm;
     a.pl = attn->pl;
     a.po = attn->po;
-    a.gm = attn->gm;
-    a.gl = attn->gl;
-    a.go = attn->go;
-    a.counters = attn->counters;
     a.max_units = attn->max_units;
-    a.max_groups = attn->max_groups;
-    a.max_counters = 1 + attn->max_groups;
-    CK(kv4::launch_attn(a, (cudaStream_t)stream, false));
+    CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, false));
     return ok();
 }
 

@@ -24,15 +24,14 @@
 // are a column's own, so a column's bits do not depend on its neighbours.
 //
 // Split.  An element is 64 keys at absolute positions, taken by one warp in two
-// steps of 32 with a fresh (m, l, c, output); a unit is eight elements (512 keys),
-// folded in order of position; units are joined in groups of 16 and then the groups,
-// by the last CTA to arrive, in order whoever it is.  So the bits depend on the
-// position alone, while the work is spread in one of two ways (launch_attn):
-//   wide   an element per warp, a unit per CTA of eight warps: short caches, where
-//          there are few units and a call's time is one CTA's latency;
-//   deep   a unit per warp, four units per CTA, keys and values through a ring of the
-//          warp's own: no barrier until the CTA's end, queries prepared once per 512
-//          keys: many units.
+// steps of 32 with a fresh (m, l, c, output); a unit is four elements (256 keys),
+// folded in order of position.  A second kernel joins the units: groups of 16, then
+// the groups, in order.  So the bits depend on the position alone, while the units
+// are spread in one of two ways (launch_attn):
+//   wide   a unit per CTA of four warps, an element per warp: short caches, where a
+//          call's time is one CTA's latency;
+//   deep   a persistent grid whose warps take equal shares of the units, keys and
+//          values through a ring of the warp's own, without any barrier: many units.
 // A warp's keys come through cp.async into shared memory that no other warp reads.
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -48,13 +47,17 @@ constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
 constexpr int kElemKeys = 64;
 constexpr int kElemSteps = kElemKeys / kStepKeys;  // 2
-constexpr int kElems = 8;                          // elements of a unit
-constexpr int kUnit = kElems * kElemKeys;          // 512 keys
+constexpr int kElems = 4;                          // elements of a unit
+constexpr int kUnit = kElems * kElemKeys;          // 256 keys
 constexpr int kWideWarps = kElems;
-constexpr int kDeepWarps = 4;                      // units of a CTA
+constexpr int kDeepWarps = 4;
+constexpr int kDeepCtas = 4;                       // CTAs of an SM
 constexpr int kDeepStages = 2;                     // steps of a deep warp's ring
-constexpr int kFan = 16;                           // units (then groups of units) joined at a time
-constexpr long kDeepUnits = 1000;                  // (unit, KV head) pairs of a call from which units go to single warps
+constexpr int kFan = 16;                           // units joined at a time
+constexpr int kJoinWarps = 16;
+constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
+constexpr int kMaxJoinBytes = ((1 << 20) / kUnit + kFan - 1) / kFan * kGroupBytes;
+constexpr long kDeepUnits = 2000;                  // units of a call (over KV heads) from which they go to single warps
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
@@ -132,12 +135,6 @@ template <int NT>
 struct Elem {
     float m[NT][2], l[NT][2], c[NT][2], za[NT][2][2];  // l and za: this lane's keys only
     float o[NT][8][4];                                 // sums over codes, in units of c and of the codes
-};
-
-// A unit's fold of its elements.
-template <int NT>
-struct Fold {
-    float M[NT][2], L[NT][2], Z[NT][2][2];
 };
 
 template <int NT>
@@ -497,366 +494,459 @@ __device__ __forceinline__ float4 finish4(float4 O, int d, const float (&z)[2]) 
     return make_float4(fmaf(O.x, k, z[0]), fmaf(O.y, k, z[1]), fmaf(O.z, k, z[0]), fmaf(O.w, k, z[1]));
 }
 
-// The last of `n` CTAs that call this for one counter (which returns to 0).
-__device__ __forceinline__ bool last_of(unsigned* counter, int n, int* flag) {
-    __syncthreads();  // the CTA's partials are written
-    if (threadIdx.x == 0) {
-        __threadfence();
-        *flag = atomicInc(counter, (unsigned)n - 1u) == (unsigned)n - 1u;
-        __threadfence();
-    }
-    __syncthreads();
-    return *flag != 0;
-}
-
-// Joins n partials (in order) of tile d of a set, by one warp: partial i's maxima and
-// sums at pm / pl + i * ts * 8 (eight columns), its output at po + i * ts * 256 float4.
-__device__ __forceinline__ void join(const float* pm, const float* pl, const float4* po, int d, int n, int ts,
-                                     float (&M)[2], float (&L)[2], float4& O) {
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    const float2* mp = reinterpret_cast<const float2*>(pm) + t;
-    const float2* lp = reinterpret_cast<const float2*>(pl) + t;
-    const float4* op = po + d * 32 + lane;
-    M[0] = M[1] = kUnset;
-    for (int i = 0; i < n; i += kFan) {
-        float2 m[kFan];
-#pragma unroll
-        for (int k = 0; k < kFan; ++k)
-            if (i + k < n) m[k] = __ldcg(mp + (size_t)(i + k) * ts * 4);
-#pragma unroll
-        for (int k = 0; k < kFan; ++k)
-            if (i + k < n) {
-                M[0] = fmaxf(M[0], m[k].x);
-                M[1] = fmaxf(M[1], m[k].y);
-            }
-    }
-    L[0] = L[1] = 0.f;
-    O = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kB = 8;
-    for (int i = 0; i < n; i += kB) {
-        float2 m[kB], l[kB];
-        float4 v[kB];
-#pragma unroll
-        for (int k = 0; k < kB; ++k)
-            if (i + k < n) {
-                m[k] = __ldcg(mp + (size_t)(i + k) * ts * 4);
-                l[k] = __ldcg(lp + (size_t)(i + k) * ts * 4);
-                v[k] = __ldcg(op + (size_t)(i + k) * ts * 256);
-            }
-#pragma unroll
-        for (int k = 0; k < kB; ++k)
-            if (i + k < n) {
-                const float w0 = ex2(m[k].x - M[0]), w1 = ex2(m[k].y - M[1]);
-                L[0] = fmaf(l[k].x, w0, L[0]);
-                L[1] = fmaf(l[k].y, w1, L[1]);
-                O.x = fmaf(v[k].x, w0, O.x);
-                O.y = fmaf(v[k].y, w1, O.y);
-                O.z = fmaf(v[k].z, w0, O.z);
-                O.w = fmaf(v[k].w, w1, O.w);
-            }
-    }
-}
-
-// Tile d's part of the output rows, into shared memory [column][128] bf16.
-__device__ __forceinline__ void put_out(bf16* rows, int d, float4 O, const float (&L)[2]) {
+// Tile d's part of the output: its columns' rows of dims, columns past nc left out.
+template <class Row>
+__device__ __forceinline__ void put_out(int d, float4 O, const float (&L)[2], Row row) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    bf16* o = rows + 2 * t * kHeadDim + 64 * (d >> 2) + 8 * g + (d & 3);
-    o[0] = rn(O.x / L[0]);
-    o[kHeadDim] = rn(O.y / L[1]);
-    o[4] = rn(O.z / L[0]);
-    o[kHeadDim + 4] = rn(O.w / L[1]);
+    const int dim = 64 * (d >> 2) + 8 * g + (d & 3);
+    if (bf16* o = row(2 * t)) {
+        o[dim] = rn(O.x / L[0]);
+        o[dim + 4] = rn(O.z / L[0]);
+    }
+    if (bf16* o = row(2 * t + 1)) {
+        o[dim] = rn(O.y / L[1]);
+        o[dim + 4] = rn(O.w / L[1]);
+    }
 }
 
+constexpr int kWideTiles = 8 / kWideWarps;  // tiles of the output a wide warp folds
+static_assert(kWideWarps == 4, "a wide warp's two tiles");
 constexpr int kScalars = 10;  // per lane and tile: m, l, 1/c (two each), zeros' sums (four)
 
-template <int NT, bool DEEP>
-struct Smem {
-    static constexpr int kWarpsOf = DEEP ? kDeepWarps : kWideWarps;
-    static constexpr int kBuf = DEEP ? kDeepStages * kStepBytes + NT * 4096 : kElemSteps * kStepBytes;  // a warp's
-    static constexpr int kScalarBytes = DEEP ? 0 : kWarpsOf * NT * kScalars * 32 * 4;
-    static constexpr int kOut = NT * 8 * kHeadDim * 2;
-    static constexpr int kBytes = kWarpsOf * kBuf + kScalarBytes + kOut;
+// What a (stream, KV head, columns) set of a call is.
+struct Set {
+    int s, h, c0, nc;      // columns c0 .. c0 + nc - 1 of stream s
+    int r0, pos0, nu, id;  // the stream's first row and position, its units; the set's partials
 };
-static_assert(Smem<2, false>::kBuf >= 2 * 4096, "a wide warp's output fits its buffer");
 
-// NT tiles of eight columns.
-template <int NT, bool DEEP>
-__global__ void __launch_bounds__(Smem<NT, DEEP>::kWarpsOf * 32, DEEP ? (NT == 1 ? 4 : 2) : (NT == 1 ? 2 : 1))
-    attn_kernel(const __grid_constant__ AttnArgs a) {
-    using S = Smem<NT, DEEP>;
-    constexpr int W = S::kWarpsOf;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ int flag;
+// Item `i` of the call's units in order of stream, columns, KV head, unit; returns the unit.
+template <int NT>
+__device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
     const Rows& rm = a.rows;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-    const int G = a.n_q / rm.n_kv;
-
-    // which (stream, head, columns, unit or four units)
     int s = 0;
-    while (s + 1 < rm.n_streams && (int)blockIdx.x >= a.item_start[s + 1]) ++s;
-    const int r0 = rm.row_start[s], R = rm.row_start[s + 1] - r0, pos0 = rm.pos0[s];
-    const int chunks = (R * G + NT * 8 - 1) / (NT * 8);
-    int item = blockIdx.x - a.item_start[s];
-    const int chunk = item % chunks;
-    item /= chunks;
-    const int h = item % rm.n_kv;
-    item /= rm.n_kv;
-    const int c0 = chunk * NT * 8, nc = min(NT * 8, R * G - c0);  // columns c0 .. c0 + nc - 1 of the stream
-    const int p_first = pos0 + c0 / G, p_last = pos0 + (c0 + nc - 1) / G;
-    const int nu = (pos0 + R - 1) / kUnit + 1;                    // units of the stream's items
-    const int u = DEEP ? item * kDeepWarps + warp : item;         // a warp's (a CTA's) unit
-    const int set = (a.set_start[s] + chunk) * rm.n_kv + h;       // this (stream, columns, head)
+    while (s + 1 < rm.n_streams && i >= a.item_start[s + 1]) ++s;
+    const int R = rm.row_start[s + 1] - rm.row_start[s];
+    i -= a.item_start[s];
+    x.s = s;
+    x.r0 = rm.row_start[s];
+    x.pos0 = rm.pos0[s];
+    x.nu = (x.pos0 + R - 1) / kUnit + 1;
+    const int u = i % x.nu, sh = i / x.nu, chunk = sh / rm.n_kv;
+    x.h = sh % rm.n_kv;
+    x.c0 = chunk * NT * 8;
+    x.nc = min(NT * 8, R * G - x.c0);
+    x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
+    return u;
+}
 
-    char* buf = smem + warp * S::kBuf;
-    bf16* rows = reinterpret_cast<bf16*>(smem + S::kBytes - S::kOut);
-    const View& kv = rm.kv[s];
-    const char* heads = kv.pages + ((size_t)rm.layer * kv.n_pages * rm.n_kv + h) * kTileBytes;
-    auto src_of = [&](int page, int k) {  // the step from key k, on a physical page
-        return heads + (size_t)page * rm.n_kv * kTileBytes + (k % kPage) / kBlockPos * kBlockBytes;
-    };
+template <int NT>
+__device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u) {
+    return ((size_t)x.id * a.max_units + u) * NT;
+}
 
+// The output row of a set's column, nullptr past the last.
+__device__ __forceinline__ bf16* out_row(const AttnArgs& a, const Set& x, int G, int col) {
+    const int c = x.c0 + col;
+    return col < x.nc ? a.out + (long)(x.r0 + c / G) * a.ldo + (x.h * G + c % G) * kHeadDim : nullptr;
+}
+
+// Wide: a unit per CTA, an element per warp.
+template <int NT>
+struct Wide {
+    static constexpr int kBuf = kElemSteps * kStepBytes;  // a warp's keys, then its output
+    static constexpr int kBytes = kWideWarps * kBuf + kWideWarps * NT * kScalars * 32 * 4;
+};
+static_assert(Wide<2>::kBuf >= 2 * 4096, "a warp's output fits its buffer");
+
+template <int NT>
+__global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 4 : 2) wide_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int W = kWideWarps;
+    extern __shared__ __align__(128) char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int G = a.n_q / a.rows.n_kv;
+    Set x;
+    const int u = find<NT>(a, G, blockIdx.x, x);
+    const int p_first = x.pos0 + x.c0 / G, p_last = x.pos0 + (x.c0 + x.nc - 1) / G;
+    const int k0 = u * kUnit + warp * kElemKeys;
+    const int steps = k0 > p_last ? 0 : min(kElemSteps, (p_last - k0) / kStepKeys + 1);
+    char* buf = smem + warp * Wide<NT>::kBuf;
     Query<NT> q;
     Elem<NT> e;
-    float* pm = a.pm + ((size_t)set * a.max_units + u) * NT * 8;
-    float* pl = a.pl + ((size_t)set * a.max_units + u) * NT * 8;
-    float4* po = reinterpret_cast<float4*>(a.po) + ((size_t)set * a.max_units + u) * NT * 256;
     pdl_wait();
-
-    if (!DEEP) {
-        const int k0 = u * kUnit + warp * kElemKeys;
-        const int steps = k0 > p_last ? 0 : min(kElemSteps, (p_last - k0) / kStepKeys + 1);
-        if (steps) {
-            const int page = __ldg(kv.table + k0 / kPage);
-            copy_step(buf, src_of(page, k0));
-            wm::cp_async_commit();
-            if (steps > 1) copy_step(buf + kStepBytes, src_of(page, k0 + kStepKeys));
-            wm::cp_async_commit();
-        }
-        load_query(q, a, r0, G, h, c0, nc, pos0);
-        if (steps) {
-            wm::cp_async_wait<1>();
-            __syncwarp();
-            any_step<NT, true>(e, q, buf, k0, p_first);
-        } else {
-            reset(e);
-        }
-        if (steps > 1) {
-            wm::cp_async_wait<0>();
-            __syncwarp();
-            any_step<NT, false>(e, q, buf + kStepBytes, k0 + kStepKeys, p_first);
-        }
-        // ---- fold the elements: every warp puts its own down and takes tile `warp` of all ----
-        float* sc = reinterpret_cast<float*>(smem + W * S::kBuf);  // [element][tile][scalar][lane]
-        __syncwarp();  // the warp has read its keys
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float4* o = reinterpret_cast<float4*>(buf) + nt * 256 + lane;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) o[d * 32] = make_float4(e.o[nt][d][0], e.o[nt][d][1], e.o[nt][d][2], e.o[nt][d][3]);
-            float* x = sc + (warp * NT + nt) * kScalars * 32 + lane;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                x[(0 + j) * 32] = e.m[nt][j];
-                x[(2 + j) * 32] = e.l[nt][j];
-                x[(4 + j) * 32] = 1.f / e.c[nt][j];
-                x[(6 + j) * 32] = e.za[nt][j][0];
-                x[(8 + j) * 32] = e.za[nt][j][1];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2] = {0.f, 0.f};
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float* x = sc + (w * NT + nt) * kScalars * 32 + lane;
-                const float4 v = *(reinterpret_cast<const float4*>(smem + w * S::kBuf) + nt * 256 + warp * 32 + lane);
-                float al[2], be[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    fold_max(M[j], x[(0 + j) * 32], al[j], be[j]);
-                    L[j] = fmaf(x[(2 + j) * 32], be[j], L[j] * al[j]);
-                    Z[j] = fmaf(x[(warp < 4 ? 6 + j : 8 + j) * 32], be[j], Z[j] * al[j]);
-                    be[j] *= x[(4 + j) * 32];
-                }
-                const float o[4] = {v.x, v.y, v.z, v.w};
-                O = fold4(O, o, al, be);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                L[j] = col_sum(L[j]);
-                Z[j] = col_sum(Z[j]);
-            }
-            O = finish4(O, warp, Z);
-            if (nu == 1) {
-                put_out(rows + nt * 8 * kHeadDim, warp, O, L);
-            } else {
-                po[nt * 256 + warp * 32 + lane] = O;
-                if (warp == 0 && lane < 4) {
-                    *reinterpret_cast<float2*>(pm + nt * 8 + 2 * t) = make_float2(M[0], M[1]);
-                    *reinterpret_cast<float2*>(pl + nt * 8 + 2 * t) = make_float2(L[0], L[1]);
-                }
-            }
-        }
-    } else {
-        const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
-        const int steps = k1 > k0 ? (k1 - k0 + kStepKeys - 1) / kStepKeys : 0;
-        int pages = 0;  // lane i: physical page of the unit's page i
-        if (steps && lane < kUnit / kPage && k0 + lane * kPage < k1) pages = __ldg(kv.table + k0 / kPage + lane);
-        auto fetch = [&](int i) {
-            if (i < steps) {
-                const int k = k0 + i * kStepKeys;
-                copy_step(buf + (i % kDeepStages) * kStepBytes,
-                          src_of(__shfl_sync(0xffffffffu, pages, (k - k0) / kPage), k));
-            }
-            wm::cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kDeepStages; ++i) fetch(i);
-        load_query(q, a, r0, G, h, c0, nc, pos0);
-        Fold<NT> f;
-        float4* O = reinterpret_cast<float4*>(buf + kDeepStages * kStepBytes) + lane;  // the fold's output [tile][8][lane]
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f.M[nt][j] = kUnset;
-                f.L[nt][j] = f.Z[nt][j][0] = f.Z[nt][j][1] = 0.f;
-            }
-#pragma unroll
-            for (int d = 0; d < 8; ++d) O[(nt * 8 + d) * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        static_assert(kElemSteps == 2 && kDeepStages == 2, "the loop's two steps and stages");
-        for (int i = 0; i < steps; i += 2) {
-            const int k = k0 + i * kStepKeys;
-            wm::cp_async_wait<1>();
-            __syncwarp();
-            any_step<NT, true>(e, q, buf, k, p_first);
-            __syncwarp();  // the stage has been read
-            fetch(i + 2);
-            if (i + 1 < steps) {
-                wm::cp_async_wait<1>();
-                __syncwarp();
-                any_step<NT, false>(e, q, buf + kStepBytes, k + kStepKeys, p_first);
-                __syncwarp();
-            }
-            fetch(i + 3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float al[2], be[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    fold_max(f.M[nt][j], e.m[nt][j], al[j], be[j]);
-                    f.L[nt][j] = fmaf(e.l[nt][j], be[j], f.L[nt][j] * al[j]);
-                    f.Z[nt][j][0] = fmaf(e.za[nt][j][0], be[j], f.Z[nt][j][0] * al[j]);
-                    f.Z[nt][j][1] = fmaf(e.za[nt][j][1], be[j], f.Z[nt][j][1] * al[j]);
-                    be[j] *= 1.f / e.c[nt][j];
-                }
-#pragma unroll
-                for (int d = 0; d < 8; ++d) O[(nt * 8 + d) * 32] = fold4(O[(nt * 8 + d) * 32], e.o[nt][d], al, be);
-            }
-        }
-        if (u < nu) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float Z[2][2], L[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    L[j] = col_sum(f.L[nt][j]);
-                    Z[0][j] = col_sum(f.Z[nt][j][0]);
-                    Z[1][j] = col_sum(f.Z[nt][j][1]);
-                }
-#pragma unroll
-                for (int d = 0; d < 8; ++d) po[(nt * 8 + d) * 32 + lane] = finish4(O[(nt * 8 + d) * 32], d, Z[d >> 2]);
-                if (lane < 4) {
-                    *reinterpret_cast<float2*>(pm + nt * 8 + 2 * t) = make_float2(f.M[nt][0], f.M[nt][1]);
-                    *reinterpret_cast<float2*>(pl + nt * 8 + 2 * t) = make_float2(L[0], L[1]);
-                }
-            }
-        }
-    }
     pdl_trigger();
-
-    // ---- join the units: groups of kFan, then the groups ----
-    if (DEEP || nu > 1) {
-        constexpr int kPer = DEEP ? kDeepWarps : 1;  // units of a CTA (a group is whole CTAs)
-        static_assert(kFan % kDeepWarps == 0, "groups of whole CTAs");
-        const int groups = (nu + kFan - 1) / kFan;
-        const int gi = item * kPer / kFan, gn = min(kFan, nu - gi * kFan);
-        unsigned* counters = a.counters + (size_t)set * a.max_counters;
-        const int arrive = (gn + kPer - 1) / kPer;
-        if (arrive > 1) {
-            if (!last_of(counters + 1 + gi, arrive, &flag)) return;
-        } else {
-            __syncthreads();  // the other warps' partials
-        }
-        for (int level = 0; level < 2; ++level) {
-            const bool final = level == 1 || groups == 1;
-            const size_t base = level == 0 ? (size_t)set * a.max_units + gi * kFan : (size_t)set * a.max_groups;
-            const float *jm = level == 0 ? a.pm : a.gm, *jl = level == 0 ? a.pl : a.gl;
-            const float4* jo = reinterpret_cast<const float4*>(level == 0 ? a.po : a.go);
-            for (int i = warp; i < NT * 8; i += W) {
-                const int nt = i >> 3, d = i & 7;
-                float M[2], L[2];
-                float4 O;
-                join(jm + (base * NT + nt) * 8, jl + (base * NT + nt) * 8, jo + (base * NT + nt) * 256, d,
-                     level == 0 ? gn : groups, NT, M, L, O);
-                if (final) {
-                    put_out(rows + nt * 8 * kHeadDim, d, O, L);
-                } else {
-                    const size_t at = ((size_t)set * a.max_groups + gi) * NT + nt;
-                    reinterpret_cast<float4*>(a.go)[at * 256 + d * 32 + lane] = O;
-                    if (d == 0 && lane < 4) {
-                        *reinterpret_cast<float2*>(a.gm + at * 8 + 2 * t) = make_float2(M[0], M[1]);
-                        *reinterpret_cast<float2*>(a.gl + at * 8 + 2 * t) = make_float2(L[0], L[1]);
-                    }
-                }
-            }
-            if (final) break;
-            if (!last_of(counters, groups, &flag)) return;
+    if (steps) {
+        const char* src = half_block(tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h), k0, 0);
+        copy_step(buf, src);
+        wm::cp_async_commit();
+        if (steps > 1) copy_step(buf + kStepBytes, src + kStepBytes);
+        wm::cp_async_commit();
+    }
+    load_query(q, a, x.r0, G, x.h, x.c0, x.nc, x.pos0);
+    if (steps) {
+        wm::cp_async_wait<1>();
+        __syncwarp();
+        any_step<NT, true>(e, q, buf, k0, p_first);
+    } else {
+        reset(e);
+    }
+    if (steps > 1) {
+        wm::cp_async_wait<0>();
+        __syncwarp();
+        any_step<NT, false>(e, q, buf + kStepBytes, k0 + kStepKeys, p_first);
+    }
+    // ---- fold the elements: every warp puts its own down and takes two tiles of all ----
+    float* sc = reinterpret_cast<float*>(smem + W * Wide<NT>::kBuf);  // [element][tile][scalar][lane]
+    __syncwarp();  // the warp has read its keys
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float4* o = reinterpret_cast<float4*>(buf) + nt * 256 + lane;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[d * 32] = make_float4(e.o[nt][d][0], e.o[nt][d][1], e.o[nt][d][2], e.o[nt][d][3]);
+        float* y = sc + (warp * NT + nt) * kScalars * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            y[(0 + j) * 32] = e.m[nt][j];
+            y[(2 + j) * 32] = e.l[nt][j];
+            y[(4 + j) * 32] = 1.f / e.c[nt][j];
+            y[(6 + j) * 32] = e.za[nt][j][0];
+            y[(8 + j) * 32] = e.za[nt][j][1];
         }
     }
-    // ---- rows of dims, out ----
     __syncthreads();
-    for (int i = threadIdx.x; i < nc * 16; i += W * 32) {  // (column, 16 bytes)
-        const int c = c0 + i / 16;
-        *reinterpret_cast<uint4*>(a.out + (long)(r0 + c / G) * a.ldo + (h * G + c % G) * kHeadDim + i % 16 * 8) =
-            *reinterpret_cast<const uint4*>(rows + i / 16 * kHeadDim + i % 16 * 8);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+        float4 O[kWideTiles];
+#pragma unroll
+        for (int k = 0; k < kWideTiles; ++k) O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float* y = sc + (w * NT + nt) * kScalars * 32 + lane;
+            float al[2], be[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                fold_max(M[j], y[(0 + j) * 32], al[j], be[j]);
+                L[j] = fmaf(y[(2 + j) * 32], be[j], L[j] * al[j]);
+                Z[0][j] = fmaf(y[(6 + j) * 32], be[j], Z[0][j] * al[j]);
+                Z[1][j] = fmaf(y[(8 + j) * 32], be[j], Z[1][j] * al[j]);
+                be[j] *= y[(4 + j) * 32];
+            }
+#pragma unroll
+            for (int k = 0; k < kWideTiles; ++k) {
+                const float4 v = *(reinterpret_cast<const float4*>(smem + w * Wide<NT>::kBuf) + nt * 256 +
+                                   (warp + k * W) * 32 + lane);
+                const float o[4] = {v.x, v.y, v.z, v.w};
+                O[k] = fold4(O[k], o, al, be);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            L[j] = col_sum(L[j]);
+            Z[0][j] = col_sum(Z[0][j]);
+            Z[1][j] = col_sum(Z[1][j]);
+        }
+        const size_t at = partial<NT>(a, x, u) + nt;
+#pragma unroll
+        for (int k = 0; k < kWideTiles; ++k) {
+            const int d = warp + k * W;
+            O[k] = finish4(O[k], d, Z[k]);  // W = 4: tiles 0..3 are of group 0, 4..7 of group 1
+            if (x.nu == 1)
+                put_out(d, O[k], L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
+            else
+                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O[k];
+        }
+        if (x.nu > 1 && warp == 0 && lane < 4) {
+            *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * t) = make_float2(M[0], M[1]);
+            *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * t) = make_float2(L[0], L[1]);
+        }
     }
 }
 
-template <int NT, bool DEEP>
-cudaError_t init_one() {
-    return cudaFuncSetAttribute(attn_kernel<NT, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<NT, DEEP>::kBytes);
+// Deep: a persistent grid; each warp takes an equal share of the call's units, one
+// after the other, with the next steps' keys always on their way, and meets no other warp.
+constexpr int kDeepBuf = kDeepStages * kStepBytes + 4096;  // a warp's ring and its fold's output
+
+__global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(128) char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int n_kv = a.rows.n_kv, G = a.n_q / n_kv;
+    // the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
+    // neighbouring shares, so that their sum differs by at most one unit between schedulers
+    const int sms = gridDim.x / kDeepCtas;
+    const long share = ((long)(blockIdx.x % sms) * kDeepWarps + warp) * kDeepCtas + blockIdx.x / sms;
+    const long shares = (long)gridDim.x * kDeepWarps;
+    const int items = a.item_start[a.rows.n_streams];
+    int i = (int)(share * items / shares);
+    const int end = (int)((share + 1) * items / shares);
+    pdl_wait();
+    pdl_trigger();
+    if (i >= end) return;
+
+    char* buf = smem + warp * kDeepBuf;
+    float4* O = reinterpret_cast<float4*>(buf + kDeepStages * kStepBytes) + lane;  // [tile][lane]
+    Set x;
+    int u = find<1>(a, G, i, x);
+    // the fetching side: its unit, step in it and what addresses need
+    int fi = i, fu = u, fstep = 0, flast, fpages;  // flast: the set's last position
+    const int* ftable;
+    const char* fheads;
+    auto open_set = [&](const Set& y) {
+        const View& kv = a.rows.kv[y.s];
+        flast = y.pos0 + (y.nc - 1) / G;
+        ftable = kv.table;
+        fheads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
+    };
+    auto open_unit = [&]() {  // lane i: physical page of the unit's page i
+        fpages = 0;
+        if (fu * kUnit + lane * kPage <= flast && lane < kUnit / kPage) fpages = __ldg(ftable + fu * (kUnit / kPage) + lane);
+    };
+    open_set(x);
+    open_unit();
+    int fslot = 0;
+    auto fetch = [&]() {
+        if (fi < end) {
+            const int k = fstep * kStepKeys;
+            const int page = __shfl_sync(0xffffffffu, fpages, k / kPage);
+            copy_step(buf + fslot * kStepBytes,
+                      fheads + (size_t)page * n_kv * kTileBytes + k % kPage / kBlockPos * kBlockBytes);
+            ++fstep;
+            if (fstep == kUnit / kStepKeys || fu * kUnit + fstep * kStepKeys > flast) {  // the next unit
+                fstep = 0;
+                if (++fi < end) {
+                    if (fu * kUnit + kUnit <= flast) {
+                        ++fu;
+                    } else {
+                        Set y;
+                        fu = find<1>(a, G, fi, y);
+                        open_set(y);
+                    }
+                    open_unit();
+                }
+            }
+        }
+        wm::cp_async_commit();
+        fslot ^= 1;
+    };
+    static_assert(kElemSteps == 2 && kDeepStages == 2, "the loop's two steps and stages");
+    fetch();
+    fetch();
+    int slot = 0;
+    Query<1> q;
+    Elem<1> e;
+    load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+    while (true) {
+        const int p_first = x.pos0, p_last = x.pos0 + (x.nc - 1) / G;
+        const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
+        float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int d = 0; d < 8; ++d) O[d * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = k0; k < k1; k += kElemKeys) {
+            wm::cp_async_wait<1>();
+            __syncwarp();
+            any_step<1, true>(e, q, buf + slot * kStepBytes, k, p_first);
+            __syncwarp();  // the stage has been read
+            fetch();
+            slot ^= 1;
+            if (k + kStepKeys < k1) {
+                wm::cp_async_wait<1>();
+                __syncwarp();
+                any_step<1, false>(e, q, buf + slot * kStepBytes, k + kStepKeys, p_first);
+                __syncwarp();
+                fetch();
+                slot ^= 1;
+            }
+            float al[2], be[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                fold_max(M[j], e.m[0][j], al[j], be[j]);
+                L[j] = fmaf(e.l[0][j], be[j], L[j] * al[j]);
+                Z[0][j] = fmaf(e.za[0][j][0], be[j], Z[0][j] * al[j]);
+                Z[1][j] = fmaf(e.za[0][j][1], be[j], Z[1][j] * al[j]);
+                be[j] *= 1.f / e.c[0][j];
+            }
+#pragma unroll
+            for (int d = 0; d < 8; ++d) O[d * 32] = fold4(O[d * 32], e.o[0][d], al, be);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            L[j] = col_sum(L[j]);
+            Z[0][j] = col_sum(Z[0][j]);
+            Z[1][j] = col_sum(Z[1][j]);
+        }
+        const size_t at = partial<1>(a, x, u);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+            const float4 v = finish4(O[d * 32], d, Z[d >> 2]);
+            if (x.nu == 1)
+                put_out(d, v, L, [&](int col) { return out_row(a, x, G, col); });
+            else
+                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = v;
+        }
+        if (x.nu > 1 && lane < 4) {
+            *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * t) = make_float2(M[0], M[1]);
+            *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * t) = make_float2(L[0], L[1]);
+        }
+        if (++i >= end) break;
+        if (u + 1 < x.nu) {
+            ++u;
+        } else {
+            u = find<1>(a, G, i, x);
+            load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+        }
+    }
+    wm::cp_async_wait_all();
+}
+
+// Joins n <= kFan partials of one tile in order, by one warp.  Partial i's eight maxima
+// and sums are at pm, pl + i * stride * 8, this lane's output at po + i * stride * 256; all
+// loads are in flight at once.  Lane 8 a + c holds column c of partials a, a + 4, ...
+__device__ __forceinline__ void join(const float* pm, const float* pl, const float4* po, int n, int stride,
+                                     float (&M)[2], float (&L)[2], float4& O) {
+    const int lane = threadIdx.x & 31, t = lane & 3, c = lane & 7, a = lane >> 3;
+    constexpr int kR = kFan / 4;
+    float m[kR], l[kR];
+    float4 v[kFan];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const bool in = 4 * r + a < n;
+        m[r] = in ? __ldcg(pm + (size_t)(4 * r + a) * stride * 8 + c) : kUnset;
+        l[r] = in ? __ldcg(pl + (size_t)(4 * r + a) * stride * 8 + c) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kFan; ++i)
+        if (i < n) v[i] = __ldcg(po + (size_t)i * stride * 256);
+    float top = m[0];
+#pragma unroll
+    for (int r = 1; r < kR; ++r) top = fmaxf(top, m[r]);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+    for (int r = 0; r < kR; ++r) m[r] = ex2(m[r] - top);  // the partial's weight
+    L[0] = L[1] = 0.f;
+    O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kFan; ++i)
+        if (i < n) {
+            const int from = (i & 3) * 8 + 2 * t;
+            const float w0 = __shfl_sync(0xffffffffu, m[i >> 2], from), w1 = __shfl_sync(0xffffffffu, m[i >> 2], from + 1);
+            L[0] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from), w0, L[0]);
+            L[1] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from + 1), w1, L[1]);
+            O.x = fmaf(v[i].x, w0, O.x);
+            O.y = fmaf(v[i].y, w1, O.y);
+            O.z = fmaf(v[i].z, w0, O.z);
+            O.w = fmaf(v[i].w, w1, O.w);
+        }
+    M[0] = __shfl_sync(0xffffffffu, top, 2 * t);
+    M[1] = __shfl_sync(0xffffffffu, top, 2 * t + 1);
+}
+
+// One tile (of a set's NT * 8) per CTA: its warps join groups of kFan units, warp 0 the
+// groups.  A group's loads are all in flight at once, so the kernel costs about two
+// round trips to the L2, however many units.
+template <int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(16) float4 js[];  // [group]: 32 x float4 output, then 8 + 8 maxima and sums
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int G = a.n_q / a.rows.n_kv;
+    // the tile's set: the item of its unit 0
+    const int tile_of = blockIdx.x % (NT * 8), set = blockIdx.x / (NT * 8);
+    const int nt = tile_of >> 3, d = tile_of & 7;
+    int s = 0;
+    while (s + 1 < a.rows.n_streams && set >= a.set_start[s + 1] * a.rows.n_kv) ++s;
+    const int R = a.rows.row_start[s + 1] - a.rows.row_start[s];
+    const int nu_s = (a.rows.pos0[s] + R - 1) / kUnit + 1;
+    Set x;
+    find<NT>(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
+    if (x.nu == 1 || nt * 8 >= x.nc) return;  // written already, or no columns
+    const int groups = (x.nu + kFan - 1) / kFan;
+    constexpr int kGroup4 = 36;  // float4 of a group
+    pdl_wait();
+    pdl_trigger();
+    float M[2], L[2];
+    float4 O;
+    for (int gi = warp; gi < groups; gi += blockDim.x / 32) {
+        const size_t at = partial<NT>(a, x, gi * kFan) + nt;
+        join(a.pm + at * 8, a.pl + at * 8, reinterpret_cast<const float4*>(a.po) + at * 256 + d * 32 + lane,
+             min(kFan, x.nu - gi * kFan), NT, M, L, O);
+        if (groups > 1) {
+            js[gi * kGroup4 + lane] = O;
+            float2* ml = reinterpret_cast<float2*>(js + gi * kGroup4 + 32);
+            if (lane < 4) {
+                ml[t] = make_float2(M[0], M[1]);
+                ml[4 + t] = make_float2(L[0], L[1]);
+            }
+        }
+    }
+    if (groups > 1) {
+        __syncthreads();
+        if (warp) return;
+        M[0] = M[1] = kUnset;
+        for (int gi = 0; gi < groups; ++gi) {
+            const float2 m = reinterpret_cast<const float2*>(js + gi * kGroup4 + 32)[t];
+            M[0] = fmaxf(M[0], m.x);
+            M[1] = fmaxf(M[1], m.y);
+        }
+        L[0] = L[1] = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int gi = 0; gi < groups; ++gi) {
+            const float2* ml = reinterpret_cast<const float2*>(js + gi * kGroup4 + 32);
+            const float2 m = ml[t], l = ml[4 + t];
+            const float4 v = js[gi * kGroup4 + lane];
+            const float w0 = ex2(m.x - M[0]), w1 = ex2(m.y - M[1]);
+            L[0] = fmaf(l.x, w0, L[0]);
+            L[1] = fmaf(l.y, w1, L[1]);
+            O.x = fmaf(v.x, w0, O.x);
+            O.y = fmaf(v.y, w1, O.y);
+            O.z = fmaf(v.z, w0, O.z);
+            O.w = fmaf(v.w, w1, O.w);
+        }
+    } else if (warp) {
+        return;
+    }
+    put_out(d, O, L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
+}
+
+cudaLaunchConfig_t cfg(int grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = attr;
+        c.numAttrs = 1;
+    }
+    return c;
+}
+
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace
 
 int attn_unit() { return kUnit; }
-int attn_fan() { return kFan; }
 
 cudaError_t init_attn() {
-    cudaError_t e = init_one<1, false>();
-    if (e == cudaSuccess) e = init_one<2, false>();
-    if (e == cudaSuccess) e = init_one<1, true>();
+    cudaError_t e = allow_smem(wide_kernel<1>, Wide<1>::kBytes);
+    if (e == cudaSuccess) e = allow_smem(wide_kernel<2>, Wide<2>::kBytes);
+    if (e == cudaSuccess) e = allow_smem(deep_kernel, kDeepWarps * kDeepBuf);
+    if (e == cudaSuccess) e = allow_smem(join_kernel<1>, kMaxJoinBytes);
+    if (e == cudaSuccess) e = allow_smem(join_kernel<2>, kMaxJoinBytes);
     return e;
 }
 
-cudaError_t launch_attn(AttnArgs& a, cudaStream_t st, bool pdl) {
+cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
     const Rows& m = a.rows;
     const int G = a.n_q / m.n_kv;
     // one tile of eight columns where every stream's rows fit it, else two: codes are then unpacked once for 16 columns
-    int nt = 1;
-    long units = 0;
-    for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s];
-        if (R * G > 8) nt = 2;
-        if (R > 0) units += (long)m.n_kv * ((m.pos0[s] + R - 1) / kUnit + 1);
-    }
-    const bool deep = nt == 1 && units >= kDeepUnits;
+    int nt = 1, most = 1;
+    for (int s = 0; s < m.n_streams; ++s)
+        if ((m.row_start[s + 1] - m.row_start[s]) * G > 8) nt = 2;
     int items = 0, sets = 0;
     for (int s = 0; s < m.n_streams; ++s) {
         const int R = m.row_start[s + 1] - m.row_start[s];
@@ -866,24 +956,23 @@ cudaError_t launch_attn(AttnArgs& a, cudaStream_t st, bool pdl) {
         sets += chunks;
         if (R > 0) {
             const int nu = (m.pos0[s] + R - 1) / kUnit + 1;
-            items += chunks * m.n_kv * (deep ? (nu + kDeepWarps - 1) / kDeepWarps : nu);
+            items += chunks * m.n_kv * nu;
+            if (nu > most) most = nu;
         }
     }
     a.item_start[m.n_streams] = items;
+    const bool deep = nt == 1 && items >= kDeepUnits;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)items);
-    c.blockDim = dim3((deep ? kDeepWarps : kWideWarps) * 32);
-    c.dynamicSmemBytes = deep ? Smem<1, true>::kBytes : nt == 1 ? Smem<1, false>::kBytes : Smem<2, false>::kBytes;
-    c.stream = st;
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        c.attrs = attr;
-        c.numAttrs = 1;
-    }
-    if (deep) return cudaLaunchKernelEx(&c, attn_kernel<1, true>, a);
-    return nt == 1 ? cudaLaunchKernelEx(&c, attn_kernel<1, false>, a) : cudaLaunchKernelEx(&c, attn_kernel<2, false>, a);
+    cudaLaunchConfig_t c = deep ? cfg(sms * kDeepCtas, kDeepWarps * 32, kDeepWarps * kDeepBuf, st, attr, pdl)
+                                : cfg(items, kWideWarps * 32, nt == 1 ? Wide<1>::kBytes : Wide<2>::kBytes, st, attr, pdl);
+    cudaError_t e = deep      ? cudaLaunchKernelEx(&c, deep_kernel, a)
+                    : nt == 1 ? cudaLaunchKernelEx(&c, wide_kernel<1>, a)
+                              : cudaLaunchKernelEx(&c, wide_kernel<2>, a);
+    if (e != cudaSuccess || most == 1) return e;
+    const int groups = (most + kFan - 1) / kFan;
+    c = cfg(sets * m.n_kv * nt * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
+            st, attr, st != nullptr);  // no programmatic launch on the legacy stream
+    return nt == 1 ? cudaLaunchKernelEx(&c, join_kernel<1>, a) : cudaLaunchKernelEx(&c, join_kernel<2>, a);
 }
 
 }  // namespace kv4
