@@ -91,9 +91,10 @@ struct ReadArgs {
     Rows rows;
     bf16 *k, *v;         // row r at k + r * ld
     long ld;
+    int item_start[kMaxStreams + 1];  // set by launch_read: first (block, head) of a stream
 };
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st, bool pdl);
-cudaError_t launch_read(const ReadArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_read(ReadArgs& a, cudaStream_t st, bool pdl);
 
 struct AttnArgs {
     Rows rows;
@@ -106,7 +107,8 @@ struct AttnArgs {
     // [set][unit][column of the set's tiles], outputs [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
     float *pm, *pl, *po;
     int max_units;
-    int item_start[kMaxStreams + 1];  // set by launch_attn: first unit (over its sets) of a stream,
+    int group;           // set by launch_attn: query heads per KV head,
+    int item_start[kMaxStreams + 1]; // first unit (over its sets) of a stream,
     int set_start[kMaxStreams];       // and its first set of columns
 };
 int attn_unit();         // keys of one partial

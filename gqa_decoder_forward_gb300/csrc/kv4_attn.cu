@@ -23,12 +23,12 @@
 // of the largest.  Likewise m moves only when an x_t passes it by 8.  Both decisions
 // are a column's own, so a column's bits do not depend on its neighbours.
 //
-// Split.  An element is 64 keys at absolute positions, taken by one warp in two
-// steps of 32 with a fresh (m, l, c, output); a unit is four elements (256 keys),
+// Split.  An element is 128 keys at absolute positions, taken by one warp in four
+// steps of 32 with a fresh (m, l, c, output); a unit is two elements (256 keys),
 // folded in order of position.  A second kernel joins the units: groups of 16, then
 // the groups, in order.  So the bits depend on the position alone, while the units
 // are spread in one of two ways (launch_attn):
-//   wide   a unit per CTA of four warps, an element per warp: short caches, where a
+//   wide   a unit per CTA, an element per warp: short caches, where a
 //          call's time is one CTA's latency;
 //   deep   a persistent grid whose warps take equal shares of the units, keys and
 //          values through a ring of the warp's own, without any barrier: many units.
@@ -45,14 +45,21 @@ namespace {
 
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
-constexpr int kElemKeys = 64;
-constexpr int kElemSteps = kElemKeys / kStepKeys;  // 2
-constexpr int kElems = 4;                          // elements of a unit
-constexpr int kUnit = kElems * kElemKeys;          // 256 keys
+#ifndef ELEM
+#define ELEM 128
+#endif
+constexpr int kElemKeys = ELEM;
+constexpr int kElemSteps = kElemKeys / kStepKeys;  // 4
+constexpr int kUnit = 256;
+constexpr int kElems = kUnit / kElemKeys;          // elements of a unit
 constexpr int kWideWarps = kElems;
 constexpr int kDeepWarps = 4;
-constexpr int kDeepCtas = 4;                       // CTAs of an SM
-constexpr int kDeepStages = 2;                     // steps of a deep warp's ring
+#ifndef DC
+#define DC 3
+#define DS 4
+#endif
+constexpr int kDeepCtas = DC;                       // CTAs of an SM
+constexpr int kDeepStages = DS;                     // steps of a deep warp's ring
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
@@ -90,14 +97,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same with c = 0 before.
-__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%10,%10,%10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+// Operands of a word's eight codes (bytes of two): "lo" the low codes of bytes 0 and 2
+// (lo[0]) and 1 and 3 (lo[1]), "both" the whole bytes, "hi" = both - lo the high codes,
+// 16 n.  The subtraction and the byte selection cost less of the half-rate logic pipe
+// than a shift and four masks.
+struct Codes {
+    uint32_t lo[2], both[2];
+};
+__device__ __forceinline__ Codes codes(uint32_t x) {
+    Codes c;
+    c.both[0] = x & 0x00ff00ffu;
+    c.both[1] = __byte_perm(x, 0, 0x4341);
+    c.lo[0] = x & 0x000f000fu;
+    c.lo[1] = c.both[1] & 0x000f000fu;
+    return c;
+}
+__device__ __forceinline__ uint32_t hi_codes(uint32_t both, uint32_t lo) {
+    uint32_t h;
+    asm("sub.u32 %0, %1, %2;" : "=r"(h) : "r"(both), "r"(lo));
+    return h;
 }
 
 // Key (0..15) of row r of a step's 16-row tiles.  With this order and the cache's
@@ -134,7 +152,7 @@ struct Query {
 template <int NT>
 struct Elem {
     float m[NT][2], l[NT][2], c[NT][2], za[NT][2][2];  // l and za: this lane's keys only
-    float o[NT][8][4];                                 // sums over codes, in units of c and of the codes
+    float o[NT][8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
 };
 
 template <int NT>
@@ -208,11 +226,12 @@ __device__ __forceinline__ void reset(Elem<NT>& e) {
     }
 }
 
-// The 32 keys from position k0, whose two blocks are at buf.  EDGE: some column does
-// not see all of them; what it does not see takes no part, whatever its bytes.
-// FIRST: the element's first step (what e held does not matter).
-template <int NT, bool EDGE, bool FIRST>
-__device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0) {
+// The 32 keys from position k0, whose two blocks are at buf.  edge (the same for the
+// whole warp): some column does not see all of them; what it does not see takes no
+// part, whatever its bytes.  One body for both, and small: the loop around it has to
+// stay in the instruction cache.
+template <int NT>
+__device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, bool edge, bool first) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int krow = key_of_row(g);  // rows g and g + 8 of the tiles: keys krow, krow + 8
     const int k_at = krow * kRowBytes + ((t ^ (krow & 2)) << 4);
@@ -220,27 +239,26 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
     float acc[2][NT][2][4];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[b][nt][0][i] = acc[b][nt][1][i] = 0.f;
         const uint4 ka = *reinterpret_cast<const uint4*>(buf + b * kBlockBytes + k_at);
         const uint4 kc = *reinterpret_cast<const uint4*>(buf + b * kBlockBytes + k_at + 8 * kRowBytes);
         const uint32_t x[4] = {ka.x, ka.y, ka.z, ka.w}, y[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+            const Codes cx = codes(x[w]), cy = codes(y[w]);
+            const uint32_t hx0 = hi_codes(cx.both[0], cx.lo[0]), hx1 = hi_codes(cx.both[1], cx.lo[1]);
+            const uint32_t hy0 = hi_codes(cy.both[0], cy.lo[0]), hy1 = hi_codes(cy.both[1], cy.lo[1]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float(&ac)[4] = acc[b][nt][w & 1];
-                const uint32_t a0 = x[w] & 0x000f000fu, a1 = y[w] & 0x000f000fu, a2 = x8 & 0x000f000fu,
-                               a3 = y8 & 0x000f000fu;
-                if (w < 2)
-                    mma_f16_first(ac, a0, a1, a2, a3, q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
-                else
-                    mma_f16(ac, a0, a1, a2, a3, q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
-                mma_f16(ac, x[w] & 0x00f000f0u, y[w] & 0x00f000f0u, x8 & 0x00f000f0u, y8 & 0x00f000f0u,
-                        q.b[nt][2 * w + 1][0], q.b[nt][2 * w + 1][1]);
+                mma_f16(acc[b][nt][w & 1], cx.lo[0], cy.lo[0], cx.lo[1], cy.lo[1], q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
+                mma_f16(acc[b][nt][w & 1], hx0, hy0, hx1, hy1, q.b[nt][2 * w + 1][0], q.b[nt][2 * w + 1][1]);
             }
         }
     }
-    // ---- scores and weights: [block][key half] ----
+    // ---- scores and weights: [block][key half][column] ----
     const char* meta = buf + kMetaOff + krow * kMetaBytes;
     auto k_meta = [&](int b, int hk) {
         return *reinterpret_cast<const uint2*>(meta + b * kBlockBytes + hk * 8 * kMetaBytes);
@@ -249,177 +267,135 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
         return *reinterpret_cast<const uint2*>(meta + kHalfBlock + b * kBlockBytes + hk * 8 * kMetaBytes);
     };
     uint32_t wb[NT][2][2][2];  // weights' operands [block][group][key half]
-    // rows of this lane a column does not see
-    auto hidden = [&](int nt, int j, int b, int hk) { return EDGE && k0 + 16 * b + 8 * hk + krow > q.pos[nt][j]; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float x[2][2][2], ts[2][2][2];
+        // rows of this lane a column does not see
+        auto hidden = [&](int j, int b, int hk) { return k0 + 16 * b + 8 * hk + krow > q.pos[nt][j]; };
+        float p[2][2][2], raw[2][2][2], top[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int hk = 0; hk < 2; ++hk) {
                 const uint2 km = k_meta(b, hk);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    ts[b][hk][j] = fmaf(lo_f(km.y), acc[b][nt][1][2 * hk + j], lo_f(km.x) * acc[b][nt][0][2 * hk + j]);
-            }
-        // x_t of a key, less m if `less`
-        auto score = [&](int b, int hk, int j, bool less) {
-            const uint2 km = k_meta(b, hk);
-            float z = less ? fmaf(hi_f(km.x), q.Q0[nt][j], -e.m[nt][j]) : hi_f(km.x) * q.Q0[nt][j];
-            z = fmaf(hi_f(km.y), q.Q1[nt][j], z);
-            const float r = fmaf(q.F[nt][j], ts[b][hk][j], z);
-            return hidden(nt, j, b, hk) ? -INFINITY : r;
-        };
-        if (FIRST) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float high = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
-                        x[b][hk][j] = score(b, hk, j, false);
-                        high = fmaxf(high, x[b][hk][j]);
-                    }
-                high = fmaxf(col_max(high), kUnset);  // -inf (nothing seen): unset
-                e.m[nt][j] = high;
-                float ps = 0.f;
-                e.l[nt][j] = 0.f;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
-                        const uint2 vm = v_meta(b, hk);
-                        const float p = ex2(x[b][hk][j] - high);  // <= 1
-                        x[b][hk][j] = p;
-                        e.l[nt][j] += p;
-                        if (!hidden(nt, j, b, hk)) ps = fmaxf(ps, fmaxf(p * lo_f(vm.x), p * lo_f(vm.y)));
-                    }
-                ps = col_max(ps);
-                e.c[nt][j] = pow2(max(-126, min(100, 6 - exponent(ps))));
-            }
-        } else {
-            float top = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int hk = 0; hk < 2; ++hk)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x[b][hk][j] = score(b, hk, j, true);
-                        top = fmaxf(top, x[b][hk][j]);
-                    }
-            if (__any_sync(0xffffffffu, top > kLazy)) {  // m moves in the columns that a score passes by more
-#pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float raw[2][2], over = -INFINITY, high = -INFINITY;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int hk = 0; hk < 2; ++hk) {
-                            raw[b][hk] = score(b, hk, j, false);
-                            over = fmaxf(over, x[b][hk][j]);
-                            high = fmaxf(high, raw[b][hk]);
-                        }
-                    over = col_max(over);
-                    high = col_max(high);
-                    if (over > kLazy) {
-                        const float al = ex2(e.m[nt][j] - high);
-                        e.m[nt][j] = high;
-                        e.l[nt][j] *= al;
-                        e.za[nt][j][0] *= al;
-                        e.za[nt][j][1] *= al;
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) {
-                            e.o[nt][d][j] *= al;
-                            e.o[nt][d][2 + j] *= al;
-                        }
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int hk = 0; hk < 2; ++hk) x[b][hk][j] = raw[b][hk] - high;
-                    }
+                    const float ts = fmaf(lo_f(km.y), acc[b][nt][1][2 * hk + j], lo_f(km.x) * acc[b][nt][0][2 * hk + j]);
+                    const float z = fmaf(hi_f(km.y), q.Q1[nt][j], hi_f(km.x) * q.Q0[nt][j]);
+                    raw[b][hk][j] = fmaf(q.F[nt][j], ts, z);
                 }
             }
+        if (edge) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x[b][hk][j] = ex2(x[b][hk][j]);
-                        e.l[nt][j] += x[b][hk][j];
-                    }
+                    for (int j = 0; j < 2; ++j)
+                        if (hidden(j, b, hk)) raw[b][hk][j] = -INFINITY;
         }
-        // x holds the weights P; w = P c s, the zeros' sums
-        auto weights = [&](int b, int hk, bool zeros) {
+        auto weights = [&](int b, int hk) {  // w = P c s
             const uint2 vm = v_meta(b, hk);
             float w[2][2];  // [group][column]
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float p = x[b][hk][j], pc = p * e.c[nt][j];
-                const bool out = hidden(nt, j, b, hk);
-                if (zeros) {
-                    const bool start = FIRST && b == 0 && hk == 0;
-                    e.za[nt][j][0] = fmaf(p, out ? 0.f : hi_f(vm.x), start ? 0.f : e.za[nt][j][0]);
-                    e.za[nt][j][1] = fmaf(p, out ? 0.f : hi_f(vm.y), start ? 0.f : e.za[nt][j][1]);
-                }
-                w[0][j] = out ? 0.f : pc * lo_f(vm.x);
-                w[1][j] = out ? 0.f : pc * lo_f(vm.y);
+                const float pc = p[b][hk][j] * e.c[nt][j];
+                w[0][j] = pc * lo_f(vm.x);
+                w[1][j] = pc * lo_f(vm.y);
+            }
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (hidden(j, b, hk)) w[0][j] = w[1][j] = 0.f;
             }
             wb[nt][b][0][hk] = pack_half(w[0][0], w[0][1]);
             wb[nt][b][1][hk] = pack_half(w[1][0], w[1][1]);
         };
-        uint32_t top2 = 0;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int j = 0; j < 2; ++j)
+            top[j] = fmaxf(fmaxf(raw[0][0][j], raw[0][1][j]), fmaxf(raw[1][0][j], raw[1][1][j]));
+        bool move = first;
+        if (!first) {
+            uint32_t top2 = 0;
 #pragma unroll
-            for (int hk = 0; hk < 2; ++hk) {
-                weights(b, hk, true);
-                // w >= 0: fp16 order is the order of the bits
-                if (!FIRST) top2 = __vmaxu2(top2, __vmaxu2(wb[nt][b][0][hk], wb[nt][b][1][hk]));
-            }
-        // 2^15 is 0x7800 (a NaN, above it, comes here too and stays NaN)
-        if (!FIRST && __any_sync(0xffffffffu, (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu)) {
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int hk = 0; hk < 2; ++hk) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[nt][j]);
+                    weights(b, hk);
+                    // w >= 0: fp16 order is the order of the bits
+                    top2 = __vimax3_u16x2(top2, wb[nt][b][0][hk], wb[nt][b][1][hk]);
+                }
+            // 2^15 is 0x7800 (a NaN, above it, counts too and stays one)
+            move = __any_sync(0xffffffffu, top[0] > e.m[nt][0] + kLazy || top[1] > e.m[nt][1] + kLazy ||
+                                               (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
+        }
+        // A score passes m by more than 8, or a w passes 2^15: m, c and the running sums move in the
+        // columns where it does.  An element's first step sets them.
+        if (move) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float wt = 0.f, ps = 0.f;  // largest w, and largest P s 2^-20 (which cannot overflow)
+                const float high = col_max(top[j]);
+                float al = 1.f;
+                if (high > e.m[nt][j] + kLazy) {
+                    al = ex2(e.m[nt][j] - high);
+                    e.m[nt][j] = high;
+                    e.l[nt][j] *= al;
+                    e.za[nt][j][0] *= al;
+                    e.za[nt][j][1] *= al;
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int hk = 0; hk < 2; ++hk) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[nt][j]);
+                float ps = 0.f;  // largest P s 2^-20 (which cannot overflow)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int hk = 0; hk < 2; ++hk) {
                         const uint2 vm = v_meta(b, hk);
-                        const float p = x[b][hk][j], pc = p * e.c[nt][j];
-                        if (!hidden(nt, j, b, hk)) {
-                            wt = fmaxf(wt, fmaxf(pc * lo_f(vm.x), pc * lo_f(vm.y)));
-                            ps = fmaxf(ps, fmaxf(p * (lo_f(vm.x) * pow2(-20)), p * (lo_f(vm.y) * pow2(-20))));
-                        }
+                        const float x = p[b][hk][j] * (fmaxf(lo_f(vm.x), lo_f(vm.y)) * pow2(-20));
+                        if (!edge || !hidden(j, b, hk)) ps = fmaxf(ps, x);
                     }
-                wt = col_max(wt);
                 ps = col_max(ps);
-                if (wt > kTopW && ps < INFINITY) {
-                    const float nc = pow2(max(-126, min(100, 6 - 20 - exponent(ps))));
-                    const float ratio = nc * (1.f / e.c[nt][j]);  // powers of two: exact, or 0
+                if (ps * e.c[nt][j] > kTopW * pow2(-20) && ps < INFINITY) {
+                    const float c = pow2(max(-126, min(100, 6 - 20 - exponent(ps))));
+                    al *= c * (1.f / e.c[nt][j]);  // powers of two: exact, or 0
+                    e.c[nt][j] = c;
+                }
+                if (!first) {
 #pragma unroll
                     for (int d = 0; d < 8; ++d) {
-                        e.o[nt][d][j] *= ratio;
-                        e.o[nt][d][2 + j] *= ratio;
+                        e.o[nt][d][j] *= al;
+                        e.o[nt][d][2 + j] *= al;
                     }
-                    e.c[nt][j] = nc;
                 }
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int hk = 0; hk < 2; ++hk) weights(b, hk, false);
+                for (int hk = 0; hk < 2; ++hk) weights(b, hk);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr)
+            for (int hk = 0; hk < 2; ++hk) {
+                const uint2 vm = v_meta(b, hk);
+                float z[2][2] = {{hi_f(vm.x), hi_f(vm.y)}, {hi_f(vm.x), hi_f(vm.y)}};  // [column][group]
+                if (edge) {
 #pragma unroll
-                for (int hk = 0; hk < 2; ++hk) wb[nt][b][gr][hk] = wm::movmatrix_t(wb[nt][b][gr][hk]);
+                    for (int j = 0; j < 2; ++j)
+                        if (hidden(j, b, hk)) z[j][0] = z[j][1] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    e.l[nt][j] += p[b][hk][j];
+                    e.za[nt][j][0] = fmaf(p[b][hk][j], z[j][0], e.za[nt][j][0]);
+                    e.za[nt][j][1] = fmaf(p[b][hk][j], z[j][1], e.za[nt][j][1]);
+                }
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) wb[nt][b][gr][hk] = wm::movmatrix_t(wb[nt][b][gr][hk]);
+            }
     }
     // ---- code sums of the output ----
     const char* vb = buf + kHalfBlock + ((g ^ ((t & 2) << 1)) << 3);
@@ -432,38 +408,20 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
             const uint32_t e0 = gr ? v0.y : v0.x, e1 = gr ? v1.y : v1.x, e2 = gr ? v2.y : v2.x, e3 = gr ? v3.y : v3.x;
-            uint32_t x0 = __byte_perm(e0, e1, 0x5410), x1 = __byte_perm(e0, e1, 0x7632);
-            uint32_t x2 = __byte_perm(e2, e3, 0x5410), x3 = __byte_perm(e2, e3, 0x7632);
+            const uint32_t x0 = __byte_perm(e0, e1, 0x5410), x1 = __byte_perm(e0, e1, 0x7632);
+            const uint32_t x2 = __byte_perm(e2, e3, 0x5410), x3 = __byte_perm(e2, e3, 0x7632);
+            const Codes y0 = codes(x0), y1 = codes(x1), y2 = codes(x2), y3 = codes(x3);
 #pragma unroll
-            for (int n = 0; n < 4; n += 2) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float(&lo)[4] = e.o[nt][gr * 4 + n];
-                    float(&hi)[4] = e.o[nt][gr * 4 + n + 1];
-                    const uint32_t w0 = wb[nt][b][gr][0], w1 = wb[nt][b][gr][1];
-                    if (FIRST && b == 0) {
-                        mma_f16_first(lo, x0 & 0x000f000fu, x1 & 0x000f000fu, x2 & 0x000f000fu, x3 & 0x000f000fu, w0, w1);
-                        mma_f16_first(hi, x0 & 0x00f000f0u, x1 & 0x00f000f0u, x2 & 0x00f000f0u, x3 & 0x00f000f0u, w0, w1);
-                    } else {
-                        mma_f16(lo, x0 & 0x000f000fu, x1 & 0x000f000fu, x2 & 0x000f000fu, x3 & 0x000f000fu, w0, w1);
-                        mma_f16(hi, x0 & 0x00f000f0u, x1 & 0x00f000f0u, x2 & 0x00f000f0u, x3 & 0x00f000f0u, w0, w1);
-                    }
+                    mma_f16(e.o[nt][gr * 4 + 2 * i], y0.lo[i], y1.lo[i], y2.lo[i], y3.lo[i], wb[nt][b][gr][0],
+                            wb[nt][b][gr][1]);
+                    mma_f16(e.o[nt][gr * 4 + 2 * i + 1], y0.both[i], y1.both[i], y2.both[i], y3.both[i],
+                            wb[nt][b][gr][0], wb[nt][b][gr][1]);
                 }
-                x0 >>= 8;
-                x1 >>= 8;
-                x2 >>= 8;
-                x3 >>= 8;
-            }
         }
     }
-}
-
-template <int NT, bool FIRST>
-__device__ __forceinline__ void any_step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, int p_first) {
-    if (k0 + kStepKeys - 1 > p_first)
-        step<NT, true, FIRST>(e, q, buf, k0);
-    else
-        step<NT, false, FIRST>(e, q, buf, k0);
 }
 
 // The two blocks of a step from global to shared memory, by one warp.
@@ -488,6 +446,17 @@ __device__ __forceinline__ float4 fold4(float4 O, const float (&o)[4], const flo
                        fmaf(o[3], b[1], O.w * a[1]));
 }
 
+// Tile d of an element's output: of the pairs of tiles, the whole bytes less the low codes leave the high ones.
+template <int NT>
+__device__ __forceinline__ void split_bytes(Elem<NT>& e) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int d = 0; d < 8; d += 2)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e.o[nt][d + 1][k] -= e.o[nt][d][k];
+}
+
 // Tile d's output from its fold: code units, and the zeros' sums of its two columns.
 __device__ __forceinline__ float4 finish4(float4 O, int d, const float (&z)[2]) {
     const float k = (d & 1) ? kHiCode : kLoCode;
@@ -510,7 +479,7 @@ __device__ __forceinline__ void put_out(int d, float4 O, const float (&L)[2], Ro
 }
 
 constexpr int kWideTiles = 8 / kWideWarps;  // tiles of the output a wide warp folds
-static_assert(kWideWarps == 4, "a wide warp's two tiles");
+static_assert(4 % kWideWarps == 0, "a wide warp's tiles");
 constexpr int kScalars = 10;  // per lane and tile: m, l, 1/c (two each), zeros' sums (four)
 
 // What a (stream, KV head, columns) set of a call is.
@@ -530,9 +499,10 @@ __device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
     x.s = s;
     x.r0 = rm.row_start[s];
     x.pos0 = rm.pos0[s];
-    x.nu = (x.pos0 + R - 1) / kUnit + 1;
-    const int u = i % x.nu, sh = i / x.nu, chunk = sh / rm.n_kv;
-    x.h = sh % rm.n_kv;
+    x.nu = (int)((unsigned)(x.pos0 + R - 1) / kUnit) + 1;
+    const unsigned sh = (unsigned)i / (unsigned)x.nu, chunk = sh / (unsigned)rm.n_kv;
+    const int u = i - (int)sh * x.nu;
+    x.h = sh - chunk * rm.n_kv;
     x.c0 = chunk * NT * 8;
     x.nc = min(NT * 8, R * G - x.c0);
     x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
@@ -551,6 +521,20 @@ __device__ __forceinline__ bf16* out_row(const AttnArgs& a, const Set& x, int G,
 }
 
 // Wide: a unit per CTA, an element per warp.
+// Step i of the kElemSteps that a warp asked for, one after the other, is there.
+__device__ __forceinline__ void wait_step(int i) {
+    static_assert(kElemSteps <= 4, "one case each");
+    if (i == kElemSteps - 1)
+        wm::cp_async_wait<0>();
+    else if (i == kElemSteps - 2)
+        wm::cp_async_wait<1>();
+    else if (i == kElemSteps - 3)
+        wm::cp_async_wait<2>();
+    else
+        wm::cp_async_wait<3>();
+    __syncwarp();
+}
+
 template <int NT>
 struct Wide {
     static constexpr int kBuf = kElemSteps * kStepBytes;  // a warp's keys, then its output
@@ -559,11 +543,11 @@ struct Wide {
 static_assert(Wide<2>::kBuf >= 2 * 4096, "a warp's output fits its buffer");
 
 template <int NT>
-__global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 4 : 2) wide_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kWideWarps * 32, (NT == 1 ? 16 : 8) / kWideWarps) wide_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int W = kWideWarps;
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-    const int G = a.n_q / a.rows.n_kv;
+    const int G = a.group;
     Set x;
     const int u = find<NT>(a, G, blockIdx.x, x);
     const int p_first = x.pos0 + x.c0 / G, p_last = x.pos0 + (x.c0 + x.nc - 1) / G;
@@ -576,27 +560,24 @@ __global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 4 : 2) wide_kernel(
     pdl_trigger();
     if (steps) {
         const char* src = half_block(tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h), k0, 0);
-        copy_step(buf, src);
-        wm::cp_async_commit();
-        if (steps > 1) copy_step(buf + kStepBytes, src + kStepBytes);
-        wm::cp_async_commit();
+#pragma unroll
+        for (int i = 0; i < kElemSteps; ++i) {
+            if (i < steps) copy_step(buf + i * kStepBytes, src + i * kStepBytes);
+            wm::cp_async_commit();
+        }
     }
     load_query(q, a, x.r0, G, x.h, x.c0, x.nc, x.pos0);
-    if (steps) {
-        wm::cp_async_wait<1>();
-        __syncwarp();
-        any_step<NT, true>(e, q, buf, k0, p_first);
-    } else {
-        reset(e);
-    }
-    if (steps > 1) {
-        wm::cp_async_wait<0>();
-        __syncwarp();
-        any_step<NT, false>(e, q, buf + kStepBytes, k0 + kStepKeys, p_first);
+    reset(e);
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+        wait_step(i);
+        const int k = k0 + i * kStepKeys;
+        step(e, q, buf + i * kStepBytes, k, k + kStepKeys - 1 > p_first, i == 0);
     }
     // ---- fold the elements: every warp puts its own down and takes two tiles of all ----
     float* sc = reinterpret_cast<float*>(smem + W * Wide<NT>::kBuf);  // [element][tile][scalar][lane]
     __syncwarp();  // the warp has read its keys
+    split_bytes(e);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float4* o = reinterpret_cast<float4*>(buf) + nt * 256 + lane;
@@ -649,7 +630,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 4 : 2) wide_kernel(
 #pragma unroll
         for (int k = 0; k < kWideTiles; ++k) {
             const int d = warp + k * W;
-            O[k] = finish4(O[k], d, Z[k]);  // W = 4: tiles 0..3 are of group 0, 4..7 of group 1
+            O[k] = finish4(O[k], d, Z[k * W / 4]);  // W <= 4: tiles 0..3 are of group 0, 4..7 of group 1
             if (x.nu == 1)
                 put_out(d, O[k], L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
             else
@@ -664,12 +645,19 @@ __global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 4 : 2) wide_kernel(
 
 // Deep: a persistent grid; each warp takes an equal share of the call's units, one
 // after the other, with the next steps' keys always on their way, and meets no other warp.
-constexpr int kDeepBuf = kDeepStages * kStepBytes + 4096;  // a warp's ring and its fold's output
+struct Fetch {
+    const char* next;                 // the step to fetch
+    const char* page[kUnit / kPage];  // the unit's pages
+    int left, in_page;                // its steps not yet fetched, and those fetched of the first page
+    int item, unit;
+};
+constexpr int kDeepBuf = kDeepStages * kStepBytes + 64;  // a warp's ring, Fetch
+static_assert(sizeof(Fetch) <= 64, "Fetch");
 
 __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-    const int n_kv = a.rows.n_kv, G = a.n_q / n_kv;
+    const int n_kv = a.rows.n_kv, G = a.group;
     // the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
     // neighbouring shares, so that their sum differs by at most one unit between schedulers
     const int sms = gridDim.x / kDeepCtas;
@@ -683,78 +671,82 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
     if (i >= end) return;
 
     char* buf = smem + warp * kDeepBuf;
-    float4* O = reinterpret_cast<float4*>(buf + kDeepStages * kStepBytes) + lane;  // [tile][lane]
     Set x;
     int u = find<1>(a, G, i, x);
-    // the fetching side: its unit, step in it and what addresses need
-    int fi = i, fu = u, fstep = 0, flast, fpages;  // flast: the set's last position
-    const int* ftable;
-    const char* fheads;
-    auto open_set = [&](const Set& y) {
+    bool fresh = false;  // another set's queries are to be loaded
+    Query<1> q;
+    load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);  // before the keys: they would wait behind them
+    // The fetching side, up to kDeepStages steps ahead, in shared memory (registers are what this kernel lacks).
+    Fetch* f = reinterpret_cast<Fetch*>(buf + kDeepStages * kStepBytes);
+    auto open = [&](int unit_i, int v, const Set& y) {
         const View& kv = a.rows.kv[y.s];
-        flast = y.pos0 + (y.nc - 1) / G;
-        ftable = kv.table;
-        fheads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
+        const int last = y.pos0 + (y.nc - 1) / G;
+        const int steps = min(kUnit, last + 1 - v * kUnit);
+        const char* heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
+        if (lane == 0) {
+            f->item = unit_i;
+            f->unit = v;
+            f->left = (steps + kStepKeys - 1) / kStepKeys;
+#pragma unroll
+            for (int p = 0; p < kUnit / kPage; ++p)
+                if (p * kPage < steps)
+                    f->page[p] = heads + (size_t)__ldg(kv.table + v * (kUnit / kPage) + p) * n_kv * kTileBytes;
+            f->next = f->page[0];
+            f->in_page = 0;
+        }
+        __syncwarp();
     };
-    auto open_unit = [&]() {  // lane i: physical page of the unit's page i
-        fpages = 0;
-        if (fu * kUnit + lane * kPage <= flast && lane < kUnit / kPage) fpages = __ldg(ftable + fu * (kUnit / kPage) + lane);
-    };
-    open_set(x);
-    open_unit();
+    open(i, u, x);
     int fslot = 0;
     auto fetch = [&]() {
-        if (fi < end) {
-            const int k = fstep * kStepKeys;
-            const int page = __shfl_sync(0xffffffffu, fpages, k / kPage);
-            copy_step(buf + fslot * kStepBytes,
-                      fheads + (size_t)page * n_kv * kTileBytes + k % kPage / kBlockPos * kBlockBytes);
-            ++fstep;
-            if (fstep == kUnit / kStepKeys || fu * kUnit + fstep * kStepKeys > flast) {  // the next unit
-                fstep = 0;
-                if (++fi < end) {
-                    if (fu * kUnit + kUnit <= flast) {
-                        ++fu;
-                    } else {
-                        Set y;
-                        fu = find<1>(a, G, fi, y);
-                        open_set(y);
-                    }
-                    open_unit();
-                }
+        if (f->left > 0) {
+            copy_step(buf + fslot * kStepBytes, f->next);
+            __syncwarp();
+            if (lane == 0) {
+                const bool turn = ++f->in_page == kPage / kStepKeys;
+                f->next = turn ? f->page[1] : f->next + kStepBytes;
+                --f->left;
+            }
+            __syncwarp();
+            const int after = f->left == 0 ? f->item + 1 : end;
+            __syncwarp();
+            if (after < end) {
+                Set y;
+                const int v = find<1>(a, G, after, y);
+                open(after, v, y);
             }
         }
         wm::cp_async_commit();
-        fslot ^= 1;
+        if (++fslot == kDeepStages) fslot = 0;
     };
-    static_assert(kElemSteps == 2 && kDeepStages == 2, "the loop's two steps and stages");
-    fetch();
-    fetch();
+    static_assert(kUnit == 2 * kPage, "one turn of a page in a unit");
+#pragma unroll 1
+    for (int k = 0; k < kDeepStages; ++k) fetch();
     int slot = 0;
-    Query<1> q;
     Elem<1> e;
-    load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+#pragma unroll 1
     while (true) {
+        if (fresh) load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+        fresh = false;
         const int p_first = x.pos0, p_last = x.pos0 + (x.nc - 1) / G;
         const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
         float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+        float4 O[8];
 #pragma unroll
-        for (int d = 0; d < 8; ++d) O[d * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = k0; k < k1; k += kElemKeys) {
-            wm::cp_async_wait<1>();
-            __syncwarp();
-            any_step<1, true>(e, q, buf + slot * kStepBytes, k, p_first);
-            __syncwarp();  // the stage has been read
-            fetch();
-            slot ^= 1;
-            if (k + kStepKeys < k1) {
-                wm::cp_async_wait<1>();
+        for (int d = 0; d < 8; ++d) O[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k = k0; k < k1;) {
+            reset(e);
+#pragma unroll 1
+            for (int i = 0; i < kElemSteps && k < k1; ++i, k += kStepKeys) {
+                wm::cp_async_wait<kDeepStages - 1>();
                 __syncwarp();
-                any_step<1, false>(e, q, buf + slot * kStepBytes, k + kStepKeys, p_first);
-                __syncwarp();
+                step(e, q, buf + slot * kStepBytes, k, k + kStepKeys - 1 > p_first, i == 0);
+                __syncwarp();  // the stage has been read
                 fetch();
-                slot ^= 1;
+                if (++slot == kDeepStages) slot = 0;
             }
+            split_bytes(e);
             float al[2], be[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -765,7 +757,7 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
                 be[j] *= 1.f / e.c[0][j];
             }
 #pragma unroll
-            for (int d = 0; d < 8; ++d) O[d * 32] = fold4(O[d * 32], e.o[0][d], al, be);
+            for (int d = 0; d < 8; ++d) O[d] = fold4(O[d], e.o[0][d], al, be);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -776,7 +768,7 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
         const size_t at = partial<1>(a, x, u);
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-            const float4 v = finish4(O[d * 32], d, Z[d >> 2]);
+            const float4 v = finish4(O[d], d, Z[d >> 2]);
             if (x.nu == 1)
                 put_out(d, v, L, [&](int col) { return out_row(a, x, G, col); });
             else
@@ -791,7 +783,7 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
             ++u;
         } else {
             u = find<1>(a, G, i, x);
-            load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+            fresh = true;
         }
     }
     wm::cp_async_wait_all();
@@ -847,7 +839,7 @@ template <int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) float4 js[];  // [group]: 32 x float4 output, then 8 + 8 maxima and sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-    const int G = a.n_q / a.rows.n_kv;
+    const int G = a.group;
     // the tile's set: the item of its unit 0
     const int tile_of = blockIdx.x % (NT * 8), set = blockIdx.x / (NT * 8);
     const int nt = tile_of >> 3, d = tile_of & 7;
@@ -942,7 +934,7 @@ cudaError_t init_attn() {
 cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
     const Rows& m = a.rows;
-    const int G = a.n_q / m.n_kv;
+    const int G = a.group = a.n_q / m.n_kv;
     // one tile of eight columns where every stream's rows fit it, else two: codes are then unpacked once for 16 columns
     int nt = 1, most = 1;
     for (int s = 0; s < m.n_streams; ++s)
@@ -971,7 +963,7 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (e != cudaSuccess || most == 1) return e;
     const int groups = (most + kFan - 1) / kFan;
     c = cfg(sets * m.n_kv * nt * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
-            st, attr, st != nullptr);  // no programmatic launch on the legacy stream
+            st, attr, true);
     return nt == 1 ? cudaLaunchKernelEx(&c, join_kernel<1>, a) : cudaLaunchKernelEx(&c, join_kernel<2>, a);
 }
 

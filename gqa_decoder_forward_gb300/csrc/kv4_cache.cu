@@ -1,8 +1,13 @@
 // Writing rows into the 4-bit cache and reading them back (layout and formula:
-// kv4.cuh).  Sixteen lanes take one (row, head) of keys or values: a lane loads
-// eight bf16 numbers (16 bytes), eight lanes find their group's minimum and
-// maximum by shuffles, and each lane writes one 32-bit word of codes; the read
-// goes the other way.
+// kv4.cuh).  Both are bound by the bytes of the dense side (256 of a row of 128 bf16
+// numbers against 72 held), so a lane moves 16 dense bytes at a time and keeps
+// several rows in flight.
+//
+// Write: sixteen lanes take one (row, head) of keys or values: a lane loads eight
+// bf16 numbers, eight lanes find their group's minimum and maximum by shuffles, and
+// each lane writes one 32-bit word of codes.
+// Read: a warp takes 16 positions of a block (1,152 contiguous bytes of the cache,
+// half a block), a half warp a row at a time; a lane holds one word of eight rows.
 #include "kv4.cuh"
 
 namespace tfl {
@@ -11,12 +16,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kItems = kThreads / 16;  // (row, head) items of a CTA
+constexpr float kRound = 12582912.f;   // 1.5 * 2^23
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
     pdl_wait();
+    pdl_trigger();
     const int kind = blockIdx.y;
     const long item = (long)blockIdx.x * kItems + threadIdx.x / 16;
     const int lane = threadIdx.x & 15;
@@ -27,8 +34,8 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     const int s = stream_of(a.rows, r);
     const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
     const long src = a.wrap ? 2l * kPage * s + pos % kPage : r;
-    const bf16* x = (kind ? a.v : a.k) + src * a.ld + (long)h * kHeadDim + lane * 8;
-    const uint4 raw = *reinterpret_cast<const uint4*>(x);
+    const bf16* x8 = (kind ? a.v : a.k) + src * a.ld + (long)h * kHeadDim + lane * 8;
+    const uint4 raw = *reinterpret_cast<const uint4*>(x8);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float f[8];
 #pragma unroll
@@ -57,10 +64,25 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     const float sc = bf(scale);
     uint32_t code = 0;
     if (!bad && sc > 0.f) {
+        // n = round_half_even((x - zero) / scale) by the reciprocal, as the low bits of 1.5 2^23 + n.  The
+        // quotient's error, 2^-21 of at most 16, can only change n within 2^-17 of a half: there, and for
+        // scales whose reciprocal overflows or that are so coarse that n could pass 15, the lane divides.
+        const float r = 1.f / sc;
+        bool near = !(sc >= 1.17549435e-38f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = fminf(rintf((f[i] - mn) / sc), 15.f);  // f >= mn: not below 0
-            code |= (uint32_t)q << (4 * i);
+            const float d = f[i] - mn, u = fmaf(d, r, kRound), rest = fmaf(kRound - u, sc, d);
+            near |= !(fabsf(rest) < 0.4999f * sc);
+            code |= (__float_as_uint(u) & 15u) << (4 * i);
+        }
+        if (near) {
+            code = 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const float x = bf(x8[i]);  // read again: the lanes that come here are few
+                const float q = fminf(rintf((x - mn) / sc), 15.f);  // x >= mn: not below 0
+                code |= (uint32_t)q << (4 * i);
+            }
         }
     }
     if (live) {
@@ -73,7 +95,6 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
                 sb | (zb << 16);
         }
     }
-    pdl_trigger();
 }
 
 // Two bf16 numbers, each z + s n rounded once to fp32 and then to bf16.
@@ -83,34 +104,48 @@ __device__ __forceinline__ uint32_t two(uint32_t code, int i, float s, float z) 
     return *reinterpret_cast<uint32_t*>(&p);
 }
 
+// A warp per (block that a stream's rows touch, head, keys or values).
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
     pdl_wait();
-    const int kind = blockIdx.y;
-    const long item = (long)blockIdx.x * kItems + threadIdx.x / 16;
-    const int lane = threadIdx.x & 15;
-    if (item < (long)a.rows.n_rows * a.rows.n_kv) {
-        const int r = (int)(item / a.rows.n_kv), h = (int)(item % a.rows.n_kv);
-        const int s = stream_of(a.rows, r);
-        const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
-        const char* hb = half_block(tile(a.rows.kv[s], a.rows.layer, a.rows.n_kv, pos, h), pos, kind);
-        const uint32_t code = *reinterpret_cast<const uint32_t*>(hb + word_at(pos, lane & 7, lane >> 3));
-        const uint32_t m =
-            *reinterpret_cast<const uint32_t*>(hb + kMetaOff + (pos % kBlockPos) * kMetaBytes + (lane >> 3) * 4);
-        const float sc = lo_f(m), z = hi_f(m);
-        uint4 o;
-        o.x = two(code, 0, sc, z);
-        o.y = two(code, 1, sc, z);
-        o.z = two(code, 2, sc, z);
-        o.w = two(code, 3, sc, z);
-        *reinterpret_cast<uint4*>((kind ? a.v : a.k) + (long)r * a.ld + (long)h * kHeadDim + lane * 8) = o;
-    }
     pdl_trigger();
+    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 7, j = (lane >> 3) & 1;
+    const int n_kv = a.rows.n_kv;
+    int item = (int)((blockIdx.x * kThreads + threadIdx.x) / 32);
+    const int kind = item & 1;
+    item >>= 1;
+    int s = 0;
+    while (s + 1 < a.rows.n_streams && item >= a.item_start[s + 1]) ++s;
+    item -= a.item_start[s];
+    if (s == a.rows.n_streams - 1 && item >= a.item_start[s + 1] - a.item_start[s]) return;
+    const int h = (int)((unsigned)item % (unsigned)n_kv), b = (int)((unsigned)item / (unsigned)n_kv);
+    const int r0 = a.rows.row_start[s], pos0 = a.rows.pos0[s], end = pos0 + a.rows.row_start[s + 1] - r0;
+    const int p0 = pos0 / kBlockPos * kBlockPos + b * kBlockPos;  // the block's first position
+    const char* hb = half_block(tile(a.rows.kv[s], a.rows.layer, n_kv, p0, h), p0, kind);
+    uint32_t code[8], meta[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // rows i * 2 + half: what was never written is read but not used
+        const int r = 2 * i + half;
+        code[i] = __ldcs(reinterpret_cast<const uint32_t*>(hb + word_at(r, c, j)));
+        meta[i] = __ldg(reinterpret_cast<const uint32_t*>(hb + kMetaOff + r * kMetaBytes + j * 4));
+    }
+    bf16* out = (kind ? a.v : a.k) + (long)h * kHeadDim + j * 64 + c * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int p = p0 + 2 * i + half;
+        if (p < pos0 || p >= end) continue;
+        const float sc = lo_f(meta[i]), z = hi_f(meta[i]);
+        uint4 o;
+        o.x = two(code[i], 0, sc, z);
+        o.y = two(code[i], 1, sc, z);
+        o.z = two(code[i], 2, sc, z);
+        o.w = two(code[i], 3, sc, z);
+        __stcs(reinterpret_cast<uint4*>(out + (long)(r0 + p - pos0) * a.ld), o);
+    }
 }
 
-cudaLaunchConfig_t cfg(const Rows& r, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
+cudaLaunchConfig_t cfg(long blocks, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
     cudaLaunchConfig_t c = {};
-    const long n = (long)r.n_rows * r.n_kv;
-    c.gridDim = dim3((unsigned)((n + kItems - 1) / kItems), 2);
+    c.gridDim = dim3((unsigned)blocks);
     c.blockDim = dim3(kThreads);
     c.stream = st;
     if (pdl) {
@@ -127,14 +162,23 @@ cudaLaunchConfig_t cfg(const Rows& r, cudaStream_t st, cudaLaunchAttribute* attr
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = cfg(a.rows, st, attr, pdl);
+    const long items = (long)a.rows.n_rows * a.rows.n_kv;
+    cudaLaunchConfig_t c = cfg((items + kItems - 1) / kItems, st, attr, pdl);
+    c.gridDim.y = 2;
     return cudaLaunchKernelEx(&c, write_kernel, a);
 }
 
-cudaError_t launch_read(const ReadArgs& a, cudaStream_t st, bool pdl) {
+cudaError_t launch_read(ReadArgs& a, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
+    int items = 0;
+    for (int s = 0; s < a.rows.n_streams; ++s) {
+        const int R = a.rows.row_start[s + 1] - a.rows.row_start[s], p = a.rows.pos0[s];
+        a.item_start[s] = items;
+        if (R > 0) items += ((p + R - 1) / kBlockPos - p / kBlockPos + 1) * a.rows.n_kv;
+    }
+    a.item_start[a.rows.n_streams] = items;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = cfg(a.rows, st, attr, pdl);
+    cudaLaunchConfig_t c = cfg(((long)items * 2 * 32 + kThreads - 1) / kThreads, st, attr, pdl);
     return cudaLaunchKernelEx(&c, read_kernel, a);
 }
 

@@ -568,13 +568,19 @@ def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:
     return st[0] if sh[0] > 1 else heads * 128
 
 
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The stream to enqueue on: torch's current one of the tensor's device if none is given (looked up without
+    making a Stream object, which would cost as much as a launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else _stream(stream)
+
+
 def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
     """Quantises rows k, v into the caches of batch."""
     ld = _rows_arg(k, batch.total, batch.n_kv)
     if _rows_arg(v, batch.total, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
     return _check(lib().tfl_kv4_write(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
-                                      v.data_ptr(), ld, _stream(stream)))
+                                      v.data_ptr(), ld, _stream_of(k, stream)))
 
 
 def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -583,7 +589,7 @@ def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, s
     if _rows_arg(v, batch.total, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
     return _check(lib().tfl_kv4_read(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
-                                     v.data_ptr(), ld, _stream(stream)))
+                                     v.data_ptr(), ld, _stream_of(k, stream)))
 
 
 def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.Tensor, out: torch.Tensor,
@@ -592,4 +598,4 @@ def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.T
     ldq = _rows_arg(q, batch.total, attn.n_q)
     ldo = _rows_arg(out, batch.total, attn.n_q)
     return _check(lib().tfl_kv4_attention(attn.handle, batch.handles, batch.n, layer, batch.pos0, batch.rows,
-                                          q.data_ptr(), ldq, out.data_ptr(), ldo, _stream(stream)))
+                                          q.data_ptr(), ldq, out.data_ptr(), ldo, _stream_of(q, stream)))

@@ -498,3 +498,28 @@ def test_many_units_on_single_warps_equal_few_units_on_whole_ctas():
         w = attend(few, [kv8], [p - 1], [2], q8)                       # two tiles
         for i in range(2):
             assert (attend(few, [kv8], [p - 1 + i], [1], q8[i: i + 1])[0] == w[i]).all()
+
+
+def test_codes_next_to_halves_and_of_every_scale():
+    """Numbers whose quotient lies on and next to a half, at scales over the whole range: the codes of the fp32 division."""
+    r = np.random.default_rng(170)
+    n = 4000
+    x = np.zeros((n, 1, 128), np.float32)
+    for i in range(n):
+        s = ref.from_bits(ref.bf16_bits(np.float32(2.0) ** r.integers(-120, 110) * np.float32(1 + r.integers(0, 128) / 128)))
+        with np.errstate(all="ignore"):
+            x[i, 0] = s * (r.integers(0, 31, 128).astype(np.float32) / 2 + r.integers(-2, 3, 128).astype(np.float32) * np.float32(2.0) ** -r.integers(4, 9))
+            x[i, 0, [0, 64]], x[i, 0, [1, 65]] = 0, 15 * s
+    x = ref.from_bits(ref.bf16_bits(x))
+    x[::2] -= 2 * np.abs(x[::2]).max(-1, keepdims=True)
+    x = ref.from_bits(ref.bf16_bits(x))
+    host, kv = make(1, 1, n)
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [n]), 0, cuda_bf16(x), cuda_bf16(-x))
+    got = ref.Cache(1, 1, n)
+    got.bytes[:] = kv.buffer.cpu().numpy()
+    for kind, y in enumerate((x, -x)):
+        a, s, z = got.get(0, n, kind)
+        code, scale, zero = ref.quantise(y)
+        np.testing.assert_array_equal(s, scale)
+        np.testing.assert_array_equal(z, zero)
+        np.testing.assert_array_equal(a, code)
