@@ -15,6 +15,7 @@
 
 #include "attn_decode.cuh"
 #include "common.cuh"
+#include "kv4.cuh"
 #include "../../include/tfl.h"
 
 using namespace tfl;
@@ -232,14 +233,14 @@ constexpr int kMaxFusedNormRows = 8;
 // Kernel families timed by tfl_profile (names in tfl_profile_kind).
 enum Kind {
     K_EMBED, K_NORM, K_QKV, K_ATTN, K_MERGE, K_O, K_GATEUP, K_DOWN, K_LMHEAD, K_ARGMAX,
-    K_GQKV, K_GO, K_GGATEUP, K_GDOWN, K_PATTN, K_STEP, K_SAMPLE, K_COUNT
+    K_GQKV, K_GO, K_GGATEUP, K_GDOWN, K_PATTN, K_STEP, K_SAMPLE, K_KV4_WRITE, K_KV4_ATTN, K_KV4_READ, K_COUNT
 };
 const char* const kKindName[K_COUNT] = {"embed_rmsnorm", "rmsnorm", "matvec_qkv_rope", "attn_decode_block",
                                         "attn_decode_merge", "matvec_o_residual", "matvec_gate_up_swiglu",
                                         "matvec_down_residual", "matvec_lm_head", "argmax",
                                         "gemm_qkv_rope", "gemm_o_residual", "gemm_gate_up_swiglu",
                                         "gemm_down_residual", "attn_prefill", "decode_step_persistent",
-                                        "sample"};
+                                        "sample", "kv4_write", "kv4_attention", "kv4_read"};
 
 struct Mark {
     int kind;
@@ -374,10 +375,19 @@ cudaError_t launch_attn_decode(const tfl_model* m, const AttnDecodeArgs& at, con
     return one_row ? launch_attn_block_tma(at, maps, m->status, m->grid, st, pdl) : launch_attn_block(at, st, pdl);
 }
 
+// A decode step over 4-bit caches: the QKV projection leaves the rows' keys and values
+// in a staging page per stream (rm's caches), from which they are quantised.
+struct Kv4Step {
+    kv4::WriteArgs write;
+    kv4::AttnArgs attn;
+    int sms;
+};
+
 // The layer stack over n rows described by rm (decode kernels).  Input: ids
-// (embedding gather) or h_in; output: the residual stream in m->h.
+// (embedding gather) or h_in; output: the residual stream in m->h.  k4: keys and
+// values go to 4-bit caches (rm holds the staging pages, maps is unused).
 int run_layers(tfl_model* m, const RowMap& rm, const KvMaps& maps, const int32_t* ids, const void* h_in,
-               cudaStream_t st) {
+               cudaStream_t st, Kv4Step* k4 = nullptr) {
     const tfl_config& c = m->cfg;
     const int n = rm.n_rows, H = c.hidden, qd = c.n_q * kHeadDim;
     const bool pdl = m->pdl && st != nullptr;  // no programmatic launch on the legacy stream
@@ -408,7 +418,7 @@ int run_layers(tfl_model* m, const RowMap& rm, const KvMaps& maps, const int32_t
         a.ldy = qd;
         a.cos_t = m->cos_t;
         a.sin_t = m->sin_t;
-        a.layer = l;
+        a.layer = k4 ? 0 : l;
         a.rows = rm;
         const int xi = xbox_index(n);
         const tfl_model::LayerMaps& wm = m->wmaps[l];
@@ -416,19 +426,25 @@ int run_layers(tfl_model* m, const RowMap& rm, const KvMaps& maps, const int32_t
         LAUNCH(m, K_QKV, st,
                mv_launch(m, a, &wm.q, &wm.k, &wm.v, &m->xmap_xn[xi], st, pdl, fuse ? m->attn_norm[l] : nullptr));
 
-        AttnDecodeArgs at = {};
-        at.q = m->q;
-        at.out = m->ao;
-        at.pm = m->pm;
-        at.pl = m->pl;
-        at.po = m->po;
-        at.max_blocks = m->L.max_blocks;
-        at.n_q = c.n_q;
-        at.n_kv = c.n_kv;
-        at.layer = l;
-        at.rows = rm;
-        LAUNCH(m, K_ATTN, st, launch_attn_decode(m, at, maps, st, pdl));
-        LAUNCH(m, K_MERGE, st, launch_attn_merge(at, st, pdl));
+        if (k4) {
+            k4->write.rows.layer = k4->attn.rows.layer = l;
+            LAUNCH(m, K_KV4_WRITE, st, kv4::launch_write(k4->write, st, pdl));
+            LAUNCH(m, K_KV4_ATTN, st, kv4::launch_attn(k4->attn, k4->sms, st, pdl));
+        } else {
+            AttnDecodeArgs at = {};
+            at.q = m->q;
+            at.out = m->ao;
+            at.pm = m->pm;
+            at.pl = m->pl;
+            at.po = m->po;
+            at.max_blocks = m->L.max_blocks;
+            at.n_q = c.n_q;
+            at.n_kv = c.n_kv;
+            at.layer = l;
+            at.rows = rm;
+            LAUNCH(m, K_ATTN, st, launch_attn_decode(m, at, maps, st, pdl));
+            LAUNCH(m, K_MERGE, st, launch_attn_merge(at, st, pdl));
+        }
 
         MatvecArgs o = {};
         o.mode = MV_RESIDUAL;
@@ -640,8 +656,15 @@ int prompt_attention(tfl_model* m, const tfl_kv* kv, const RowMap& rm, int layer
 // tcgen05 GEMM projections with fused epilogues, attention.  Each row's result
 // depends only on its own input and position, so chunk boundaries never change
 // results (a prompt resumed from a kept prefix equals the same prompt fresh).
+// k4: kv is a one-layer scratch cache with an identity table; the chunk's keys and
+// values are quantised from it, and the layer's positions read back into it before
+// the attention, so that every row attends what the 4-bit cache stands for.
+struct Kv4Prompt {
+    kv4::WriteArgs write;
+    kv4::ReadArgs read;
+};
 int run_prompt_layers(tfl_model* m, const tfl_kv* kv, const RowMap& rm, const int32_t* ids, const void* h_in,
-                      cudaStream_t st) {
+                      cudaStream_t st, Kv4Prompt* k4 = nullptr) {
     const tfl_config& c = m->cfg;
     const int n = rm.n_rows, H = c.hidden, qd = c.n_q * kHeadDim;
     const bool pdl = m->pdl && st != nullptr;
@@ -666,10 +689,15 @@ int run_prompt_layers(tfl_model* m, const tfl_kv* kv, const RowMap& rm, const in
         a.ldy = qd;
         a.cos_t = m->cos_t;
         a.sin_t = m->sin_t;
-        a.layer = l;
+        a.layer = k4 ? 0 : l;
         a.rows = rm;
         LAUNCH(m, K_GQKV, st, gemm_launch(m, a, &m->amap_xn, &wm.gq, &wm.gk, &wm.gv, st, pdl));
-        int e = prompt_attention(m, kv, rm, l, m->q, m->ao, st, pdl);
+        if (k4) {
+            k4->write.rows.layer = k4->read.rows.layer = l;
+            LAUNCH(m, K_KV4_WRITE, st, kv4::launch_write(k4->write, st, pdl));
+            LAUNCH(m, K_KV4_READ, st, kv4::launch_read(k4->read, st, pdl));
+        }
+        int e = prompt_attention(m, kv, rm, k4 ? 0 : l, m->q, m->ao, st, pdl);
         if (e) return e;
         MatvecArgs o = {};
         o.mode = MV_RESIDUAL;
@@ -724,6 +752,143 @@ int prefill_common(tfl_model* m, tfl_kv* kv, const int32_t* ids, const void* h_i
         if (e) return e;
     }
     kv->length += n_rows;
+    return ok();
+}
+
+// ---- 4-bit caches ------------------------------------------------------------------
+
+// Bytes of the staging pages of a decode step: per stream, 128 key rows and 128 value rows.
+size_t kv4_staging_bytes(const tfl_config& c) { return (size_t)2 * kPage * c.n_kv * kHeadDim * 2; }
+
+int check_kv4(const tfl_model* m, const tfl_kv4* kv, int s) {
+    if (!kv) return fail(TFL_E_ARG, "stream %d: NULL 4-bit cache", s);
+    if (kv->layers != m->cfg.layers || kv->n_kv != m->cfg.n_kv)
+        return fail(TFL_E_ARG, "stream %d: a 4-bit cache of %d layers and %d heads; the model has %d and %d", s,
+                    kv->layers, kv->n_kv, m->cfg.layers, m->cfg.n_kv);
+    int dev = -1;
+    CK(cudaGetDevice(&dev));
+    if (kv->device != dev)
+        return fail(TFL_E_ARG, "stream %d: the 4-bit cache is on device %d and the current device is %d", s, kv->device,
+                    dev);
+    return TFL_OK;
+}
+
+int decode_kv4(tfl_model* m, tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, const int32_t* ids,
+               const int* rows, void* logits, void* workspace, size_t ws_bytes, cudaStream_t st) {
+    if (!m || !attn || !kvs || !rows || !ids || !logits) return fail(TFL_E_ARG, "NULL argument");
+    const tfl_config& c = m->cfg;
+    if (n_streams < 1 || n_streams > kMaxStreams) return fail(TFL_E_ARG, "n_streams %d outside 1..16", n_streams);
+    if (attn->n_q != c.n_q || attn->n_kv != c.n_kv)
+        return fail(TFL_E_ARG, "an attention object for %d query / %d KV heads; the model has %d / %d", attn->n_q,
+                    attn->n_kv, c.n_q, c.n_kv);
+    if (!workspace || ((uintptr_t)workspace & 255u)) return fail(TFL_E_ARG, "workspace NULL or not 256-byte aligned");
+    const size_t need = tfl_kv4_step_workspace_bytes(m);
+    if (ws_bytes < need) return fail(TFL_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    RowMap rm;
+    std::memset(&rm, 0, sizeof rm);
+    Kv4Step k4;
+    std::memset(&k4, 0, sizeof k4);
+    kv4::Rows& kr = k4.write.rows;
+    int total = 0;
+    for (int s = 0; s < n_streams; ++s) {
+        const tfl_kv4* kv = kvs[s];
+        if (int e = check_kv4(m, kv, s)) return e;
+        for (int t = 0; t < s; ++t)
+            if (kvs[t] == kv) return fail(TFL_E_ARG, "stream %d repeats the KV object of stream %d", s, t);
+        if (rows[s] < 1 || rows[s] > 16) return fail(TFL_E_ARG, "stream %d: %d rows outside 1..16", s, rows[s]);
+        const int end = std::min(std::min(kv->max_pos, c.max_context), attn->max_pos);
+        if (kv->length + rows[s] > end)
+            return fail(TFL_E_CAPACITY, "stream %d: positions %d..%d reach the KV capacity %d; rejected", s, kv->length,
+                        kv->length + rows[s] - 1, end);
+        rm.row_start[s] = kr.row_start[s] = total;
+        rm.pos0[s] = kr.pos0[s] = kv->length;
+        kr.kv[s] = kv->view();
+        // the stream's staging page: one page that every position maps to (two table entries, zeros, are read)
+        rm.kv[s].pages = (bf16*)((char*)workspace + s * kv4_staging_bytes(c));
+        rm.kv[s].table = (const int*)m->zero_row - kv->length / kPage;
+        rm.kv[s].n_pages = 1;
+        total += rows[s];
+    }
+    if (total > c.max_decode_rows || total > kMaxDecodeRows || total > attn->max_rows)
+        return fail(TFL_E_ARG, "%d rows in one step exceed %d", total,
+                    std::min(std::min(c.max_decode_rows, kMaxDecodeRows), attn->max_rows));
+    rm.n_streams = kr.n_streams = n_streams;
+    rm.n_rows = kr.n_rows = rm.row_start[n_streams] = kr.row_start[n_streams] = total;
+    kr.n_kv = c.n_kv;
+    k4.write.k = (const bf16*)workspace;
+    k4.write.v = k4.write.k + (size_t)kPage * c.n_kv * kHeadDim;
+    k4.write.ld = (long)c.n_kv * kHeadDim;
+    k4.write.wrap = 1;
+    k4.attn.rows = kr;
+    k4.attn.n_q = c.n_q;
+    k4.attn.q = m->q;
+    k4.attn.out = m->ao;
+    k4.attn.ldq = k4.attn.ldo = (long)c.n_q * kHeadDim;
+    k4.attn.pm = attn->pm;
+    k4.attn.pl = attn->pl;
+    k4.attn.po = attn->po;
+    k4.attn.max_units = attn->max_units;
+    k4.sms = attn->sms;
+    KvMaps none;  // unused
+    if (int e = run_layers(m, rm, none, ids, nullptr, st, &k4)) return e;
+    if (int e = run_head(m, 0, total, logits, c.vocab, st)) return e;
+    for (int s = 0; s < n_streams; ++s) kvs[s]->length += rows[s];
+    return ok();
+}
+
+int prefill_kv4(tfl_model* m, tfl_kv4* kv, const int32_t* ids, int n_rows, void* logits, int all_rows, void* workspace,
+                size_t ws_bytes, cudaStream_t st) {
+    if (!m || !ids) return fail(TFL_E_ARG, "NULL model or ids");
+    const tfl_config& c = m->cfg;
+    if (int e = check_kv4(m, kv, 0)) return e;
+    if (n_rows < 1 || n_rows > c.max_rows) return fail(TFL_E_ARG, "n_rows %d outside 1..%d", n_rows, c.max_rows);
+    const int pos0 = kv->length, end = pos0 + n_rows;
+    if (end > kv->max_pos || end > c.max_context)
+        return fail(TFL_E_CAPACITY, "positions %d..%d reach the KV capacity %d; rejected", pos0, end - 1,
+                    std::min(kv->max_pos, c.max_context));
+    if (!workspace || ((uintptr_t)workspace & 255u)) return fail(TFL_E_ARG, "workspace NULL or not 256-byte aligned");
+    const size_t need = tfl_kv4_prompt_workspace_bytes(m, end);
+    if (ws_bytes < need) return fail(TFL_E_WORKSPACE, "workspace %zu bytes < %zu needed for %d positions", ws_bytes, need, end);
+    // a one-layer bf16 cache over the workspace
+    tfl_kv scratch = {};
+    scratch.model = m;
+    scratch.n_pages = (end + kPage - 1) / kPage;
+    scratch.max_pos = scratch.n_pages * kPage;
+    scratch.table = (int*)workspace;
+    scratch.pages = (bf16*)((char*)workspace + kv_table_bytes(scratch.n_pages));
+    if (!encode_kv_map(&scratch.kvmap, scratch.pages, c.n_kv, (uint64_t)2 * scratch.n_pages * kPage))
+        return fail(TFL_E_CUDA, "building the KV tensor map failed");
+    CK(kv4::launch_identity(scratch.table, scratch.n_pages, st));
+    RowMap rm;
+    std::memset(&rm, 0, sizeof rm);
+    rm.n_streams = 1;
+    rm.n_rows = rm.row_start[1] = n_rows;
+    rm.pos0[0] = pos0;
+    rm.kv[0] = view(&scratch);
+    Kv4Prompt k4;
+    std::memset(&k4, 0, sizeof k4);
+    const long ld = (long)c.n_kv * kHeadDim;
+    const size_t values = (size_t)scratch.max_pos * ld;
+    kv4::Rows& kr = k4.write.rows;
+    kr.n_streams = 1;
+    kr.n_kv = c.n_kv;
+    kr.n_rows = kr.row_start[1] = n_rows;
+    kr.pos0[0] = pos0;
+    kr.kv[0] = kv->view();
+    k4.write.k = scratch.pages + (size_t)pos0 * ld;
+    k4.write.v = k4.write.k + values;
+    k4.write.ld = ld;
+    k4.read.rows = kr;
+    k4.read.rows.n_rows = k4.read.rows.row_start[1] = end;
+    k4.read.rows.pos0[0] = 0;
+    k4.read.k = scratch.pages;
+    k4.read.v = scratch.pages + values;
+    k4.read.ld = ld;
+    if (int e = run_prompt_layers(m, &scratch, rm, ids, nullptr, st, &k4)) return e;
+    if (logits)
+        if (int e = all_rows ? run_head(m, 0, n_rows, logits, c.vocab, st) : run_head(m, n_rows - 1, 1, logits, c.vocab, st))
+            return e;
+    kv->length = end;
     return ok();
 }
 
@@ -1289,6 +1454,26 @@ int tfl_layer_op(tfl_model* m, int op, int layer, tfl_kv* kv, int pos0, int rows
             break;
     }
     return ok();
+}
+
+size_t tfl_kv4_step_workspace_bytes(const tfl_model* m) {
+    return m ? std::min(kMaxStreams, m->cfg.max_decode_rows) * kv4_staging_bytes(m->cfg) : 0;
+}
+
+int tfl_decode_step_kv4(tfl_model* m, tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, const int32_t* ids,
+                        const int* rows, void* logits, void* workspace, size_t ws_bytes, void* stream) {
+    return decode_kv4(m, attn, kvs, n_streams, ids, rows, logits, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t tfl_kv4_prompt_workspace_bytes(const tfl_model* m, int positions) {
+    if (!m || positions < 1 || positions > m->cfg.max_context) return 0;
+    const int n = (positions + kPage - 1) / kPage;
+    return kv_table_bytes(n) + (size_t)2 * n * kPage * m->cfg.n_kv * kHeadDim * 2;
+}
+
+int tfl_prefill_chunk_kv4(tfl_model* m, tfl_kv4* kv, const int32_t* ids, int n_rows, void* logits, int all_rows,
+                          void* workspace, size_t ws_bytes, void* stream) {
+    return prefill_kv4(m, kv, ids, n_rows, logits, all_rows, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 int tfl_profile(tfl_model* m, int enable) {

@@ -95,6 +95,7 @@ struct ReadArgs {
 };
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_read(ReadArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_identity(int* table, int n, cudaStream_t st);  // table[i] = i
 
 struct AttnArgs {
     Rows rows;

@@ -143,6 +143,11 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     }
 }
 
+__global__ void __launch_bounds__(kThreads) identity_kernel(int* table, int n) {
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (i < n) table[i] = i;
+}
+
 cudaLaunchConfig_t cfg(long blocks, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)blocks);
@@ -180,6 +185,11 @@ cudaError_t launch_read(ReadArgs& a, cudaStream_t st, bool pdl) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t c = cfg(((long)items * 2 * 32 + kThreads - 1) / kThreads, st, attr, pdl);
     return cudaLaunchKernelEx(&c, read_kernel, a);
+}
+
+cudaError_t launch_identity(int* table, int n, cudaStream_t st) {
+    identity_kernel<<<(n + kThreads - 1) / kThreads, kThreads, 0, st>>>(table, n);
+    return cudaGetLastError();
 }
 
 }  // namespace kv4

@@ -121,6 +121,12 @@ SIGNATURES = {
     "tfl_kv4_attn_free": (None, [_vp]),
     "tfl_kv4_attention": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp,
                                          ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
+    "tfl_kv4_step_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "tfl_decode_step_kv4": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_vp), ctypes.c_int, _vp, _intp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]),
+    "tfl_kv4_prompt_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
+    "tfl_prefill_chunk_kv4": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_size_t,
+                                             _vp]),
 }
 
 _lib = None
@@ -599,3 +605,46 @@ def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.T
     ldo = _rows_arg(out, batch.total, attn.n_q)
     return _check(lib().tfl_kv4_attention(attn.handle, batch.handles, batch.n, layer, batch.pos0, batch.rows,
                                           q.data_ptr(), ldq, out.data_ptr(), ldo, _stream_of(q, stream)))
+
+
+class KV4Runner:
+    """The forward of a model over 4-bit caches: the attention object and the
+    workspaces of tfl_decode_step_kv4 (up to max_rows rows) and tfl_prefill_chunk_kv4,
+    for caches of up to max_positions positions.  One call at a time."""
+
+    def __init__(self, model: Model, max_rows: int = 16, max_positions: int = 4096):
+        s = model.shape
+        self.model = model
+        self.max_positions = max_positions
+        self.attention = KV4Attention(s.n_q, s.n_kv, max_rows, max_positions)
+        self.step_ws = torch.empty(int(lib().tfl_kv4_step_workspace_bytes(model.handle)), dtype=torch.uint8,
+                                   device="cuda")
+        self.prompt_ws = torch.empty(int(lib().tfl_kv4_prompt_workspace_bytes(model.handle, max_positions)),
+                                     dtype=torch.uint8, device="cuda")
+
+    def kv(self, max_positions: int) -> KV4:
+        return KV4(self.model.shape.layers, self.model.shape.n_kv, max_positions)
+
+    def decode_step(self, kvs: Sequence[KV4], ids: torch.Tensor, rows: Sequence[int], logits: torch.Tensor,
+                    stream=None):
+        return tfl_decode_step_kv4(self, kvs, ids, rows, logits, stream)
+
+    def prefill_chunk(self, kv: KV4, ids: torch.Tensor, logits=None, all_rows=False, stream=None):
+        return tfl_prefill_chunk_kv4(self, kv, ids, logits, all_rows, stream)
+
+
+def tfl_decode_step_kv4(runner: KV4Runner, kvs, ids, rows, logits, stream=None):
+    """tfl_decode_step over 4-bit caches."""
+    assert ids.dtype == torch.int32 and logits.dtype == torch.bfloat16
+    r = (ctypes.c_int * len(rows))(*rows)
+    return _check(lib().tfl_decode_step_kv4(runner.model.handle, runner.attention.handle, _kv_array(kvs), len(kvs),
+                                            _ptr(ids), r, _ptr(logits), _ptr(runner.step_ws), runner.step_ws.numel(),
+                                            _stream(stream)))
+
+
+def tfl_prefill_chunk_kv4(runner: KV4Runner, kv: KV4, ids, logits=None, all_rows=False, stream=None):
+    """tfl_prefill_chunk into a 4-bit cache."""
+    assert ids.dtype == torch.int32
+    return _check(lib().tfl_prefill_chunk_kv4(runner.model.handle, kv.handle, _ptr(ids), ids.numel(), _ptr(logits),
+                                              1 if all_rows else 0, _ptr(runner.prompt_ws), runner.prompt_ws.numel(),
+                                              _stream(stream)))

@@ -555,6 +555,30 @@ void tfl_kv4_attn_free(tfl_kv4_attn* attn);
 int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, void* stream);
 
+/*
+ * The forward over 4-bit caches: tfl_decode_step and tfl_prefill_chunk with the
+ * keys and values held in caches of the model's layers and KV heads.  Every row,
+ * of a step, a window or a chunk, attends what the cache stands for, its own
+ * key and value among it; a chunk's attention reads those numbers rounded to bf16,
+ * a step's does not.  As in the calls on bf16 caches, a step's rows do not depend
+ * on the other rows and streams of the call, nor a prompt's on where chunks end,
+ * and lengths advance as work is enqueued.
+ *
+ * decode: attn: an object for the model's heads whose max_rows and max_positions
+ * hold the step.  prefill: one stream; reads the layer's earlier positions back
+ * into the workspace, one layer at a time.  workspace: device, 256-byte aligned,
+ * caller-owned, tfl_kv4_step_workspace_bytes(model) bytes or
+ * tfl_kv4_prompt_workspace_bytes(model, length + n_rows) bytes, its contents of no
+ * meaning between calls; calls that share one, or one attn, must not overlap on
+ * the GPU.  A launch per operation (never the one-launch step).
+ */
+size_t tfl_kv4_step_workspace_bytes(const tfl_model* model);
+int tfl_decode_step_kv4(tfl_model* model, tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, const int32_t* ids,
+                        const int* rows_per_stream, void* logits, void* workspace, size_t ws_bytes, void* stream);
+size_t tfl_kv4_prompt_workspace_bytes(const tfl_model* model, int positions);
+int tfl_prefill_chunk_kv4(tfl_model* model, tfl_kv4* kv, const int32_t* ids, int n_rows, void* logits, int all_rows,
+                          void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- per-kernel timing ------------------------------------------------------------- */
 
 /*
