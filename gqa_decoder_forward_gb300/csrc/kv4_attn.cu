@@ -56,7 +56,7 @@ constexpr int kWideWarps = kElems;
 constexpr int kDeepWarps = 4;
 #ifndef DC
 #define DC 3
-#define DS 4
+#define DS 3
 #endif
 constexpr int kDeepCtas = DC;                       // CTAs of an SM
 constexpr int kDeepStages = DS;                     // steps of a deep warp's ring
@@ -226,12 +226,12 @@ __device__ __forceinline__ void reset(Elem<NT>& e) {
     }
 }
 
-// The 32 keys from position k0, whose two blocks are at buf.  edge (the same for the
-// whole warp): some column does not see all of them; what it does not see takes no
-// part, whatever its bytes.  One body for both, and small: the loop around it has to
-// stay in the instruction cache.
-template <int NT>
-__device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, bool edge, bool first) {
+// The 32 keys from position k0, whose two blocks are at buf.  EDGE: some column does
+// not see all of them; what it does not see takes no part, whatever its bytes.
+// first: the element's first step.  (A body of its own for that costs more in
+// instruction cache misses than its tests.)
+template <int NT, bool EDGE>
+__device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, bool first) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int krow = key_of_row(g);  // rows g and g + 8 of the tiles: keys krow, krow + 8
     const int k_at = krow * kRowBytes + ((t ^ (krow & 2)) << 4);
@@ -284,7 +284,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                     raw[b][hk][j] = fmaf(q.F[nt][j], ts, z);
                 }
             }
-        if (edge) {
+        if (EDGE) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -302,7 +302,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                 w[0][j] = pc * lo_f(vm.x);
                 w[1][j] = pc * lo_f(vm.y);
             }
-            if (edge) {
+            if (EDGE) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (hidden(j, b, hk)) w[0][j] = w[1][j] = 0.f;
@@ -355,7 +355,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                     for (int hk = 0; hk < 2; ++hk) {
                         const uint2 vm = v_meta(b, hk);
                         const float x = p[b][hk][j] * (fmaxf(lo_f(vm.x), lo_f(vm.y)) * pow2(-20));
-                        if (!edge || !hidden(j, b, hk)) ps = fmaxf(ps, x);
+                        if (!EDGE || !hidden(j, b, hk)) ps = fmaxf(ps, x);
                     }
                 ps = col_max(ps);
                 if (ps * e.c[nt][j] > kTopW * pow2(-20) && ps < INFINITY) {
@@ -382,7 +382,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
             for (int hk = 0; hk < 2; ++hk) {
                 const uint2 vm = v_meta(b, hk);
                 float z[2][2] = {{hi_f(vm.x), hi_f(vm.y)}, {hi_f(vm.x), hi_f(vm.y)}};  // [column][group]
-                if (edge) {
+                if (EDGE) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         if (hidden(j, b, hk)) z[j][0] = z[j][1] = 0.f;
@@ -422,6 +422,14 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                 }
         }
     }
+}
+
+template <int NT>
+__device__ __forceinline__ void any_step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, int p_first, bool first) {
+    if (k0 + kStepKeys - 1 > p_first)
+        step<NT, true>(e, q, buf, k0, first);
+    else
+        step<NT, false>(e, q, buf, k0, first);
 }
 
 // The two blocks of a step from global to shared memory, by one warp.
@@ -571,8 +579,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, (NT == 1 ? 16 : 8) / kWideWar
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
         wait_step(i);
-        const int k = k0 + i * kStepKeys;
-        step(e, q, buf + i * kStepBytes, k, k + kStepKeys - 1 > p_first, i == 0);
+        any_step(e, q, buf + i * kStepBytes, k0 + i * kStepKeys, p_first, i == 0);
     }
     // ---- fold the elements: every warp puts its own down and takes two tiles of all ----
     float* sc = reinterpret_cast<float*>(smem + W * Wide<NT>::kBuf);  // [element][tile][scalar][lane]
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
             for (int i = 0; i < kElemSteps && k < k1; ++i, k += kStepKeys) {
                 wm::cp_async_wait<kDeepStages - 1>();
                 __syncwarp();
-                step(e, q, buf + slot * kStepBytes, k, k + kStepKeys - 1 > p_first, i == 0);
+                any_step(e, q, buf + slot * kStepBytes, k, p_first, i == 0);
                 __syncwarp();  // the stage has been read
                 fetch();
                 if (++slot == kDeepStages) slot = 0;
