@@ -45,26 +45,19 @@ namespace {
 
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
-#ifndef ELEM
-#define ELEM 128
-#endif
-constexpr int kElemKeys = ELEM;
+constexpr int kElemKeys = kPage;                   // keys of an element: a page
 constexpr int kElemSteps = kElemKeys / kStepKeys;  // 4
-constexpr int kUnit = 256;
-constexpr int kElems = kUnit / kElemKeys;          // elements of a unit
+constexpr int kElems = 2;                          // elements of a unit
+constexpr int kUnit = kElems * kElemKeys;          // 256 keys
 constexpr int kWideWarps = kElems;
 constexpr int kDeepWarps = 4;
-#ifndef DC
-#define DC 3
-#define DS 3
-#endif
-constexpr int kDeepCtas = DC;                       // CTAs of an SM
-constexpr int kDeepStages = DS;                     // steps of a deep warp's ring
+constexpr int kDeepCtas = 3;                       // CTAs of an SM
+constexpr int kDeepStages = 3;                     // steps of a deep warp's ring
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
 constexpr int kMaxJoinBytes = ((1 << 20) / kUnit + kFan - 1) / kFan * kGroupBytes;
-constexpr long kDeepUnits = 2000;                  // units of a call (over KV heads) from which they go to single warps
+constexpr int kDeepUnits = 4;                  // units of a CTA from which a call's units go to the persistent grid
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
@@ -432,6 +425,12 @@ __device__ __forceinline__ void any_step(Elem<NT>& e, const Query<NT>& q, const 
         step<NT, false>(e, q, buf, k0, first);
 }
 
+// Hand-over of an element to the warp of the quarter before: hardware barriers of the two warps.
+__device__ __forceinline__ void hand_arrive(int quarter) {
+    asm volatile("bar.arrive %0, 64;" ::"r"(quarter) : "memory");
+}
+__device__ __forceinline__ void hand_wait(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(quarter) : "memory"); }
+
 // The two blocks of a step from global to shared memory, by one warp.
 __device__ __forceinline__ void copy_step(char* dst, const char* src) {
     const int lane = threadIdx.x & 31;
@@ -441,35 +440,42 @@ __device__ __forceinline__ void copy_step(char* dst, const char* src) {
     static_assert(kStepBytes % 512 == 0, "whole rounds of 32 lanes");
 }
 
-// One element into the fold of (M) of a column: the weights of what is folded so far and of the element.
-__device__ __forceinline__ void fold_max(float& M, float m, float& a, float& b) {
-    const float n = fmaxf(M, m);
-    a = ex2(M - n);
-    b = ex2(m - n);
-    M = n;
-}
-
-__device__ __forceinline__ float4 fold4(float4 O, const float (&o)[4], const float (&a)[2], const float (&b)[2]) {
-    return make_float4(fmaf(o[0], b[0], O.x * a[0]), fmaf(o[1], b[1], O.y * a[1]), fmaf(o[2], b[0], O.z * a[0]),
-                       fmaf(o[3], b[1], O.w * a[1]));
-}
-
-// Tile d of an element's output: of the pairs of tiles, the whole bytes less the low codes leave the high ones.
+// An element's end, in place: l and the zeros' sums over the column's lanes (za[j][0]
+// becomes l's), o from code units and c to the output's own scale, zeros added.  Of the
+// pairs of tiles, the whole bytes less the low codes leave the high ones.
 template <int NT>
-__device__ __forceinline__ void split_bytes(Elem<NT>& e) {
+__device__ __forceinline__ void finish(Elem<NT>& e) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int d = 0; d < 8; d += 2)
+        for (int j = 0; j < 2; ++j) {
+            e.l[nt][j] = col_sum(e.l[nt][j]);
+            const float z[2] = {col_sum(e.za[nt][j][0]), col_sum(e.za[nt][j][1])};
+            const float inv = 1.f / e.c[nt][j];  // a power of two up to 2^126
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e.o[nt][d + 1][k] -= e.o[nt][d][k];
+            for (int d = 0; d < 8; d += 2)
+#pragma unroll
+                for (int k = j; k < 4; k += 2) {
+                    const float lo = e.o[nt][d][k], hi = e.o[nt][d + 1][k] - lo;
+                    e.o[nt][d][k] = fmaf(lo * kLoCode, inv, z[d >> 2]);
+                    e.o[nt][d + 1][k] = fmaf(hi * kHiCode, inv, z[d >> 2]);
+                }
+        }
 }
 
-// Tile d's output from its fold: code units, and the zeros' sums of its two columns.
-__device__ __forceinline__ float4 finish4(float4 O, int d, const float (&z)[2]) {
-    const float k = (d & 1) ? kHiCode : kLoCode;
-    return make_float4(fmaf(O.x, k, z[0]), fmaf(O.y, k, z[1]), fmaf(O.z, k, z[0]), fmaf(O.w, k, z[1]));
+// Joins two finished partials of a column; (kUnset, 0, 0) changes nothing.
+__device__ __forceinline__ void join_weights(float& m0, float m1, float& l0, float l1, float& w0, float& w1) {
+    const float m = fmaxf(m0, m1);
+    w0 = ex2(m0 - m);
+    w1 = ex2(m1 - m);
+    l0 = fmaf(l1, w1, l0 * w0);
+    m0 = m;
 }
+__device__ __forceinline__ float4 join4(float4 a, float4 b, const float (&w0)[2], const float (&w1)[2]) {
+    return make_float4(fmaf(b.x, w1[0], a.x * w0[0]), fmaf(b.y, w1[1], a.y * w0[1]), fmaf(b.z, w1[0], a.z * w0[0]),
+                       fmaf(b.w, w1[1], a.w * w0[1]));
+}
+__device__ __forceinline__ float4 f4(const float (&o)[4]) { return make_float4(o[0], o[1], o[2], o[3]); }
 
 // Tile d's part of the output: its columns' rows of dims, columns past nc left out.
 template <class Row>
@@ -485,10 +491,6 @@ __device__ __forceinline__ void put_out(int d, float4 O, const float (&L)[2], Ro
         o[dim + 4] = rn(O.w / L[1]);
     }
 }
-
-constexpr int kWideTiles = 8 / kWideWarps;  // tiles of the output a wide warp folds
-static_assert(4 % kWideWarps == 0, "a wide warp's tiles");
-constexpr int kScalars = 10;  // per lane and tile: m, l, 1/c (two each), zeros' sums (four)
 
 // What a (stream, KV head, columns) set of a call is.
 struct Set {
@@ -528,33 +530,41 @@ __device__ __forceinline__ bf16* out_row(const AttnArgs& a, const Set& x, int G,
     return col < x.nc ? a.out + (long)(x.r0 + c / G) * a.ldo + (x.h * G + c % G) * kHeadDim : nullptr;
 }
 
-// Wide: a unit per CTA, an element per warp.
 // Step i of the kElemSteps that a warp asked for, one after the other, is there.
 __device__ __forceinline__ void wait_step(int i) {
-    static_assert(kElemSteps <= 4, "one case each");
-    if (i == kElemSteps - 1)
-        wm::cp_async_wait<0>();
-    else if (i == kElemSteps - 2)
-        wm::cp_async_wait<1>();
-    else if (i == kElemSteps - 3)
-        wm::cp_async_wait<2>();
-    else
+    static_assert(kElemSteps == 4, "one case each");
+    if (i == 0)
         wm::cp_async_wait<3>();
+    else if (i == 1)
+        wm::cp_async_wait<2>();
+    else if (i == 2)
+        wm::cp_async_wait<1>();
+    else
+        wm::cp_async_wait<0>();
     __syncwarp();
 }
 
+// A unit's partial (one tile of columns): O by the caller's lanes, M and L by lanes 0..3.
+__device__ __forceinline__ void put_max_sum(const AttnArgs& a, size_t at, const float (&M)[2], const float (&L)[2]) {
+    const int lane = threadIdx.x & 31;
+    if (lane < 4) {
+        *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * lane) = make_float2(M[0], M[1]);
+        *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(L[0], L[1]);
+    }
+}
+
+// Wide: a unit per CTA, an element per warp.
 template <int NT>
 struct Wide {
-    static constexpr int kBuf = kElemSteps * kStepBytes;  // a warp's keys, then its output
-    static constexpr int kBytes = kWideWarps * kBuf + kWideWarps * NT * kScalars * 32 * 4;
+    static constexpr int kBuf = kElemSteps * kStepBytes;                          // a warp's keys, then its output
+    static constexpr int kBytes = kWideWarps * kBuf + kWideWarps * NT * 4 * 32 * 4;  // and its maxima and sums
 };
 static_assert(Wide<2>::kBuf >= 2 * 4096, "a warp's output fits its buffer");
 
 template <int NT>
-__global__ void __launch_bounds__(kWideWarps * 32, (NT == 1 ? 16 : 8) / kWideWarps) wide_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int W = kWideWarps;
+__global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 8 : 4) wide_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group;
     Set x;
     const int u = find<NT>(a, G, blockIdx.x, x);
@@ -567,7 +577,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, (NT == 1 ? 16 : 8) / kWideWar
     pdl_wait();
     pdl_trigger();
     if (steps) {
-        const char* src = half_block(tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h), k0, 0);
+        const char* src = tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h);
 #pragma unroll
         for (int i = 0; i < kElemSteps; ++i) {
             if (i < steps) copy_step(buf + i * kStepBytes, src + i * kStepBytes);
@@ -581,216 +591,227 @@ __global__ void __launch_bounds__(kWideWarps * 32, (NT == 1 ? 16 : 8) / kWideWar
         wait_step(i);
         any_step(e, q, buf + i * kStepBytes, k0 + i * kStepKeys, p_first, i == 0);
     }
-    // ---- fold the elements: every warp puts its own down and takes two tiles of all ----
-    float* sc = reinterpret_cast<float*>(smem + W * Wide<NT>::kBuf);  // [element][tile][scalar][lane]
+    // ---- join the two elements: every warp puts its own down and takes half the tiles of both ----
     __syncwarp();  // the warp has read its keys
-    split_bytes(e);
+    finish(e);
+    float* sc = reinterpret_cast<float*>(smem + kWideWarps * Wide<NT>::kBuf);  // [element][tile][m, l][lane]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float4* o = reinterpret_cast<float4*>(buf) + nt * 256 + lane;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) o[d * 32] = make_float4(e.o[nt][d][0], e.o[nt][d][1], e.o[nt][d][2], e.o[nt][d][3]);
-        float* y = sc + (warp * NT + nt) * kScalars * 32 + lane;
+        for (int d = 0; d < 8; ++d) o[d * 32] = f4(e.o[nt][d]);
+        float* y = sc + (warp * NT + nt) * 128 + lane;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            y[(0 + j) * 32] = e.m[nt][j];
+            y[j * 32] = e.m[nt][j];
             y[(2 + j) * 32] = e.l[nt][j];
-            y[(4 + j) * 32] = 1.f / e.c[nt][j];
-            y[(6 + j) * 32] = e.za[nt][j][0];
-            y[(8 + j) * 32] = e.za[nt][j][1];
         }
     }
     __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-        float4 O[kWideTiles];
-#pragma unroll
-        for (int k = 0; k < kWideTiles; ++k) O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float* y = sc + (w * NT + nt) * kScalars * 32 + lane;
-            float al[2], be[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                fold_max(M[j], y[(0 + j) * 32], al[j], be[j]);
-                L[j] = fmaf(y[(2 + j) * 32], be[j], L[j] * al[j]);
-                Z[0][j] = fmaf(y[(6 + j) * 32], be[j], Z[0][j] * al[j]);
-                Z[1][j] = fmaf(y[(8 + j) * 32], be[j], Z[1][j] * al[j]);
-                be[j] *= y[(4 + j) * 32];
-            }
-#pragma unroll
-            for (int k = 0; k < kWideTiles; ++k) {
-                const float4 v = *(reinterpret_cast<const float4*>(smem + w * Wide<NT>::kBuf) + nt * 256 +
-                                   (warp + k * W) * 32 + lane);
-                const float o[4] = {v.x, v.y, v.z, v.w};
-                O[k] = fold4(O[k], o, al, be);
-            }
-        }
+        const float *y0 = sc + nt * 128 + lane, *y1 = y0 + NT * 128;
+        float M[2], L[2], w0[2], w1[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            L[j] = col_sum(L[j]);
-            Z[0][j] = col_sum(Z[0][j]);
-            Z[1][j] = col_sum(Z[1][j]);
+            M[j] = y0[j * 32];
+            L[j] = y0[(2 + j) * 32];
+            join_weights(M[j], y1[j * 32], L[j], y1[(2 + j) * 32], w0[j], w1[j]);
         }
         const size_t at = partial<NT>(a, x, u) + nt;
 #pragma unroll
-        for (int k = 0; k < kWideTiles; ++k) {
-            const int d = warp + k * W;
-            O[k] = finish4(O[k], d, Z[k * W / 4]);  // W <= 4: tiles 0..3 are of group 0, 4..7 of group 1
+        for (int k = 0; k < 4; ++k) {
+            const int d = warp * 4 + k;
+            const float4* o = reinterpret_cast<const float4*>(smem) + nt * 256 + d * 32 + lane;
+            const float4 O = join4(o[0], o[Wide<NT>::kBuf / 16], w0, w1);
             if (x.nu == 1)
-                put_out(d, O[k], L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
+                put_out(d, O, L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
             else
-                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O[k];
+                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O;
         }
-        if (x.nu > 1 && warp == 0 && lane < 4) {
-            *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * t) = make_float2(M[0], M[1]);
-            *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * t) = make_float2(L[0], L[1]);
-        }
+        if (x.nu > 1 && warp == 0) put_max_sum(a, at, M, L);
     }
 }
 
-// Deep: a persistent grid; each warp takes an equal share of the call's units, one
-// after the other, with the next steps' keys always on their way, and meets no other warp.
+// Deep: a persistent grid.  A CTA takes an equal share of the call's units, its warps equal
+// shares of their elements, one element after the other with the next steps' keys always
+// on their way.  A unit whose elements fall to two warps is joined by the warp of the
+// first, at its end; the warp of the second has left its part in shared memory at its own
+// beginning, so nobody waits in practice.
 struct Fetch {
-    const char* next;                 // the step to fetch
-    const char* page[kUnit / kPage];  // the unit's pages
-    int left, in_page;                // its steps not yet fetched, and those fetched of the first page
-    int item, unit;
+    const char *next, *heads;  // the step to fetch; tile 0 of the layer and head
+    const int* table;
+    int left;                  // steps of the element not yet fetched
+    int elem, u, last;         // the element (2 x unit + half), its unit in the set, the set's last position
 };
 constexpr int kDeepBuf = kDeepStages * kStepBytes + 64;  // a warp's ring, Fetch
+static_assert(kDeepUnits >= 2, "no empty quarter");
 static_assert(sizeof(Fetch) <= 64, "Fetch");
+constexpr int kHandFloats = 1024 + 128;                  // an element handed over: output, maxima and sums
+constexpr int kDeepBytes = kDeepWarps * (kDeepBuf + kHandFloats * 4);
 
 __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_kv = a.rows.n_kv, G = a.group;
-    // the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
-    // neighbouring shares, so that their sum differs by at most one unit between schedulers
-    const int sms = gridDim.x / kDeepCtas;
-    const long share = ((long)(blockIdx.x % sms) * kDeepWarps + warp) * kDeepCtas + blockIdx.x / sms;
-    const long shares = (long)gridDim.x * kDeepWarps;
+    // units of this CTA, elements of this warp; warps take the CTA's quarters in turn from CTA to CTA, so
+    // that a scheduler (the same warp of an SM's CTAs) gets every quarter
     const int items = a.item_start[a.rows.n_streams];
-    int i = (int)(share * items / shares);
-    const int end = (int)((share + 1) * items / shares);
+    const int first = (int)((long)blockIdx.x * items / gridDim.x), last = (int)((long)(blockIdx.x + 1) * items / gridDim.x);
+    const int sms = gridDim.x / kDeepCtas, quarter = (warp + blockIdx.x / sms) % kDeepWarps, n = 2 * (last - first);
+    int v = 2 * first + quarter * n / kDeepWarps;
+    const int end = 2 * first + (quarter + 1) * n / kDeepWarps;
     pdl_wait();
     pdl_trigger();
-    if (i >= end) return;
+    // A CTA has at least two units (launch_attn), so no quarter is empty, and the quarter after one that ends
+    // with a unit's first element begins with its second.
 
     char* buf = smem + warp * kDeepBuf;
+    float* hand = reinterpret_cast<float*>(smem + kDeepWarps * kDeepBuf);  // [quarter][kHandFloats]
     Set x;
-    int u = find<1>(a, G, i, x);
-    bool fresh = false;  // another set's queries are to be loaded
-    Query<1> q;
-    load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);  // before the keys: they would wait behind them
+    int u = find<1>(a, G, v >> 1, x);
     // The fetching side, up to kDeepStages steps ahead, in shared memory (registers are what this kernel lacks).
     Fetch* f = reinterpret_cast<Fetch*>(buf + kDeepStages * kStepBytes);
-    auto open = [&](int unit_i, int v, const Set& y) {
+    auto open_set = [&](const Set& y, int unit) {  // lane 0
         const View& kv = a.rows.kv[y.s];
-        const int last = y.pos0 + (y.nc - 1) / G;
-        const int steps = min(kUnit, last + 1 - v * kUnit);
-        const char* heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
-        if (lane == 0) {
-            f->item = unit_i;
-            f->unit = v;
-            f->left = (steps + kStepKeys - 1) / kStepKeys;
-#pragma unroll
-            for (int p = 0; p < kUnit / kPage; ++p)
-                if (p * kPage < steps)
-                    f->page[p] = heads + (size_t)__ldg(kv.table + v * (kUnit / kPage) + p) * n_kv * kTileBytes;
-            f->next = f->page[0];
-            f->in_page = 0;
-        }
-        __syncwarp();
+        f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
+        f->table = kv.table;
+        f->last = y.pos0 + (y.nc - 1) / G;
+        f->u = unit;
     };
-    open(i, u, x);
+    auto open = [&](int elem) {  // lane 0
+        const int k = f->u * kUnit + (elem & 1) * kElemKeys, keys = f->last + 1 - k;
+        f->elem = elem;
+        f->left = keys <= 0 ? 0 : min(kElemSteps, (keys + kStepKeys - 1) / kStepKeys);
+        if (keys > 0) f->next = f->heads + (size_t)__ldg(f->table + k / kPage) * n_kv * kTileBytes;
+    };
+    auto open_next = [&]() {  // lane 0: the element after f->elem that has keys (a set's last unit may lack a second)
+        while (f->left == 0 && f->elem + 1 < end) {
+            const int elem = f->elem + 1;
+            if ((elem & 1) == 0) {
+                if (f->u * kUnit + kUnit <= f->last) {
+                    ++f->u;
+                } else {
+                    Set y;
+                    const int w = find<1>(a, G, elem >> 1, y);
+                    open_set(y, w);
+                }
+            }
+            open(elem);
+        }
+    };
+    if (lane == 0) {
+        open_set(x, u);
+        open(v);
+        open_next();
+    }
+    __syncwarp();
     int fslot = 0;
     auto fetch = [&]() {
         if (f->left > 0) {
             copy_step(buf + fslot * kStepBytes, f->next);
             __syncwarp();
             if (lane == 0) {
-                const bool turn = ++f->in_page == kPage / kStepKeys;
-                f->next = turn ? f->page[1] : f->next + kStepBytes;
+                f->next += kStepBytes;
                 --f->left;
+                open_next();
             }
             __syncwarp();
-            const int after = f->left == 0 ? f->item + 1 : end;
-            __syncwarp();
-            if (after < end) {
-                Set y;
-                const int v = find<1>(a, G, after, y);
-                open(after, v, y);
-            }
         }
         wm::cp_async_commit();
         if (++fslot == kDeepStages) fslot = 0;
     };
-    static_assert(kUnit == 2 * kPage, "one turn of a page in a unit");
-#pragma unroll 1
-    for (int k = 0; k < kDeepStages; ++k) fetch();
+    fetch();  // one step on its way before the queries, which would wait behind more
+    bool fresh = true;  // the set's queries are to be loaded
     int slot = 0;
+    Query<1> q;
     Elem<1> e;
+    float4 O[8];      // a unit's first element, until its second is there
+    float M[2], L[2];
+    bool held = false;
 #pragma unroll 1
     while (true) {
         if (fresh) load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
+        if (fresh && slot == 0 && fslot == 1) {
+#pragma unroll 1
+            for (int k = 1; k < kDeepStages; ++k) fetch();
+        }
         fresh = false;
         const int p_first = x.pos0, p_last = x.pos0 + (x.nc - 1) / G;
-        const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
-        float M[2] = {kUnset, kUnset}, L[2] = {0.f, 0.f}, Z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-        float4 O[8];
+        const int k0 = u * kUnit + (v & 1) * kElemKeys, k1 = min(k0 + kElemKeys, p_last + 1);
+        reset(e);
+#pragma unroll 1
+        for (int k = k0; k < k1; k += kStepKeys) {
+            wm::cp_async_wait<kDeepStages - 1>();
+            __syncwarp();
+            any_step(e, q, buf + slot * kStepBytes, k, p_first, k == k0);
+            __syncwarp();  // the stage has been read
+            fetch();
+            if (++slot == kDeepStages) slot = 0;
+        }
+        finish(e);
+        const bool second = v & 1, ends = v + 1 == end;
+        bool whole = false;  // e.o, e.m, e.l hold a whole unit
+        if (second && !held) {  // for the quarter before
+            float* h = hand + quarter * kHandFloats + lane;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) O[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int k = k0; k < k1;) {
-            reset(e);
-#pragma unroll 1
-            for (int i = 0; i < kElemSteps && k < k1; ++i, k += kStepKeys) {
-                wm::cp_async_wait<kDeepStages - 1>();
-                __syncwarp();
-                any_step(e, q, buf + slot * kStepBytes, k, p_first, i == 0);
-                __syncwarp();  // the stage has been read
-                fetch();
-                if (++slot == kDeepStages) slot = 0;
-            }
-            split_bytes(e);
-            float al[2], be[2];
+            for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(h - lane)[d * 32 + lane] = f4(e.o[0][d]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                fold_max(M[j], e.m[0][j], al[j], be[j]);
-                L[j] = fmaf(e.l[0][j], be[j], L[j] * al[j]);
-                Z[0][j] = fmaf(e.za[0][j][0], be[j], Z[0][j] * al[j]);
-                Z[1][j] = fmaf(e.za[0][j][1], be[j], Z[1][j] * al[j]);
-                be[j] *= 1.f / e.c[0][j];
+                h[1024 + j * 32] = e.m[0][j];
+                h[1024 + (2 + j) * 32] = e.l[0][j];
+            }
+            hand_arrive(quarter);
+        } else if (second || ends) {
+            float w0[2], w1[2];
+            if (second) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) join_weights(M[j], e.m[0][j], L[j], e.l[0][j], w0[j], w1[j]);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) O[d] = join4(O[d], f4(e.o[0][d]), w0, w1);
+            } else {  // a first element at the end: its second is the next quarter's first
+                const float* h = hand + (quarter + 1) * kHandFloats + lane;
+                hand_wait(quarter + 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    M[j] = e.m[0][j];
+                    L[j] = e.l[0][j];
+                    join_weights(M[j], h[1024 + j * 32], L[j], h[1024 + (2 + j) * 32], w0[j], w1[j]);
+                }
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    O[d] = join4(f4(e.o[0][d]), reinterpret_cast<const float4*>(h - lane)[d * 32 + lane], w0, w1);
+            }
+            whole = true;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                M[j] = e.m[0][j];
+                L[j] = e.l[0][j];
             }
 #pragma unroll
-            for (int d = 0; d < 8; ++d) O[d] = fold4(O[d], e.o[0][d], al, be);
+            for (int d = 0; d < 8; ++d) O[d] = f4(e.o[0][d]);
         }
+        held = !second;
+        if (whole) {
+            const size_t at = partial<1>(a, x, u);
+            if (x.nu == 1) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            L[j] = col_sum(L[j]);
-            Z[0][j] = col_sum(Z[0][j]);
-            Z[1][j] = col_sum(Z[1][j]);
-        }
-        const size_t at = partial<1>(a, x, u);
+                for (int d = 0; d < 8; ++d) put_out(d, O[d], L, [&](int col) { return out_row(a, x, G, col); });
+            } else {
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-            const float4 v = finish4(O[d], d, Z[d >> 2]);
-            if (x.nu == 1)
-                put_out(d, v, L, [&](int col) { return out_row(a, x, G, col); });
-            else
-                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = v;
+                for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O[d];
+                put_max_sum(a, at, M, L);
+            }
         }
-        if (x.nu > 1 && lane < 4) {
-            *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * t) = make_float2(M[0], M[1]);
-            *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * t) = make_float2(L[0], L[1]);
-        }
-        if (++i >= end) break;
-        if (u + 1 < x.nu) {
-            ++u;
-        } else {
-            u = find<1>(a, G, i, x);
-            fresh = true;
+        if (++v >= end) break;
+        if (second) {
+            if (u + 1 < x.nu) {
+                ++u;
+            } else {
+                u = find<1>(a, G, v >> 1, x);
+                fresh = true;
+            }
         }
     }
     wm::cp_async_wait_all();
@@ -932,7 +953,7 @@ int attn_unit() { return kUnit; }
 cudaError_t init_attn() {
     cudaError_t e = allow_smem(wide_kernel<1>, Wide<1>::kBytes);
     if (e == cudaSuccess) e = allow_smem(wide_kernel<2>, Wide<2>::kBytes);
-    if (e == cudaSuccess) e = allow_smem(deep_kernel, kDeepWarps * kDeepBuf);
+    if (e == cudaSuccess) e = allow_smem(deep_kernel, kDeepBytes);
     if (e == cudaSuccess) e = allow_smem(join_kernel<1>, kMaxJoinBytes);
     if (e == cudaSuccess) e = allow_smem(join_kernel<2>, kMaxJoinBytes);
     return e;
@@ -960,9 +981,9 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
         }
     }
     a.item_start[m.n_streams] = items;
-    const bool deep = nt == 1 && items >= kDeepUnits;
+    const bool deep = nt == 1 && items >= kDeepUnits * kDeepCtas * sms;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = deep ? cfg(sms * kDeepCtas, kDeepWarps * 32, kDeepWarps * kDeepBuf, st, attr, pdl)
+    cudaLaunchConfig_t c = deep ? cfg(sms * kDeepCtas, kDeepWarps * 32, kDeepBytes, st, attr, pdl)
                                 : cfg(items, kWideWarps * 32, nt == 1 ? Wide<1>::kBytes : Wide<2>::kBytes, st, attr, pdl);
     cudaError_t e = deep      ? cudaLaunchKernelEx(&c, deep_kernel, a)
                     : nt == 1 ? cudaLaunchKernelEx(&c, wide_kernel<1>, a)
