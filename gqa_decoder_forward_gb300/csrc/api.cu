@@ -828,6 +828,7 @@ int decode_kv4(tfl_model* m, tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_stre
     k4.attn.pl = attn->pl;
     k4.attn.po = attn->po;
     k4.attn.max_units = attn->max_units;
+    k4.attn.status = m->status;
     k4.sms = attn->sms;
     KvMaps none;  // unused
     if (int e = run_layers(m, rm, none, ids, nullptr, st, &k4)) return e;

@@ -108,6 +108,7 @@ struct AttnArgs {
     // [set][unit][column of the set's tiles], outputs [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
     float *pm, *pl, *po;
     int max_units;
+    int* status;         // device status word: a bounded wait that gives up raises kStatusDevice
     int group;           // set by launch_attn: query heads per KV head,
     int item_start[kMaxStreams + 1]; // first unit (over its sets) of a stream,
     int set_start[kMaxStreams];       // and its first set of columns
@@ -133,4 +134,5 @@ struct tfl_kv4_attn {
     int n_q, n_kv, max_rows, max_pos, max_units;
     int sms;  // of the device
     float *pm, *pl, *po;
+    int* status;
 };

@@ -63,7 +63,7 @@ bool attn_sizes_ok(int n_q, int n_kv, int head_dim, int max_rows, int max_positi
 
 // Workspace of an attention object (byte offsets, 256-byte aligned regions).
 struct AttnLayout {
-    size_t pm, pl, po, total;
+    size_t status, pm, pl, po, total;
     int units;
 };
 
@@ -80,6 +80,7 @@ AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
         off = round256(off + bytes);
         return o;
     };
+    L.status = take(256);
     L.pm = take(tiles * L.units * 8 * 4);
     L.pl = take(tiles * L.units * 8 * 4);
     L.po = take(tiles * L.units * 8 * kHeadDim * 4);
@@ -274,8 +275,24 @@ int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_pos
     a->pl = (float*)(ws + L.pl);
     a->po = (float*)(ws + L.po);
     a->sms = sms;
+    a->status = (int*)(ws + L.status);
+    const cudaError_t ce = cudaMemset(a->status, 0, 256);
+    if (ce != cudaSuccess) {
+        delete a;
+        return fail(TFL_E_CUDA, "clearing the status word failed: %s", cudaGetErrorString(ce));
+    }
     *out = a;
     return ok();
+}
+
+int tfl_kv4_attn_status(tfl_kv4_attn* attn, void* stream) {
+    if (!attn) return fail(TFL_E_ARG, "NULL attention object");
+    CK(cudaStreamSynchronize((cudaStream_t)stream));
+    int s = 0;
+    CK(cudaMemcpy(&s, attn->status, 4, cudaMemcpyDeviceToHost));
+    if (s == 0) return ok();
+    CK(cudaMemset(attn->status, 0, 4));
+    return fail(TFL_E_DEVICE, "a kernel gave up a bounded wait");
 }
 
 void tfl_kv4_attn_free(tfl_kv4_attn* attn) { delete attn; }
@@ -307,6 +324,7 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
     a.pl = attn->pl;
     a.po = attn->po;
     a.max_units = attn->max_units;
+    a.status = attn->status;
     CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, false));
     return ok();
 }

@@ -32,11 +32,13 @@
 //          call's time is one CTA's latency;
 //   deep   a persistent grid whose warps take equal shares of the units, keys and
 //          values through a ring of the warp's own, without any barrier: many units.
-// A warp's keys come through cp.async into shared memory that no other warp reads.
+// A warp's keys come by bulk copies that one of its lanes asks for, into shared memory
+// that no other warp reads.
 #include <cfloat>
 #include <cuda_fp16.h>
 
 #include "kv4.cuh"
+#include "tma.cuh"
 #include "warp_mma.cuh"
 
 namespace tfl {
@@ -69,6 +71,9 @@ __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
 __device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 0xff) - 127; }
+
+// 1 / 2^e for a power of two of -126..126 (0 and 2^127 do not come).
+__device__ __forceinline__ float inv_pow2(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -147,61 +152,6 @@ struct Elem {
     float m[NT][2], l[NT][2], c[NT][2], za[NT][2][2];  // l and za: this lane's keys only
     float o[NT][8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
 };
-
-template <int NT>
-__device__ __forceinline__ void load_query(Query<NT>& q, const AttnArgs& a, int r0, int G, int h, int c0, int nc,
-                                           int pos0) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int c = c0 + nt * 8 + g;
-        float x[4][8];
-        float amax = 0.f, sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {  // the dims of this lane's words of a key's row
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (nt * 8 + g < nc)
-                raw = *reinterpret_cast<const uint4*>(a.q + (long)(r0 + c / G) * a.ldq + (h * G + c % G) * kHeadDim +
-                                                      (w & 1) * 64 + 16 * t + (w >> 1) * 8);
-            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[w][2 * i] = lo_f(u[i]);
-                x[w][2 * i + 1] = hi_f(u[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                amax = fmaxf(amax, fabsf(x[w][i]));
-                sum[w & 1] += x[w][i];
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
-        }
-        const int e = max(-100, min(126, 13 - exponent(amax)));
-        const float up = pow2(e), up4 = pow2(e - 4);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            q.b[nt][2 * w][0] = pack_half(x[w][0] * up, x[w][4] * up);
-            q.b[nt][2 * w][1] = pack_half(x[w][2] * up, x[w][6] * up);
-            q.b[nt][2 * w + 1][0] = pack_half(x[w][1] * up4, x[w][5] * up4);
-            q.b[nt][2 * w + 1][1] = pack_half(x[w][3] * up4, x[w][7] * up4);
-        }
-        const float f = pow2(24 - e) * kLog2eOverSqrtD;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int from = (2 * t + j) * 4;
-            q.F[nt][j] = __shfl_sync(0xffffffffu, f, from);
-            q.Q0[nt][j] = __shfl_sync(0xffffffffu, sum[0] * kLog2eOverSqrtD, from);
-            q.Q1[nt][j] = __shfl_sync(0xffffffffu, sum[1] * kLog2eOverSqrtD, from);
-            const int cc = nt * 8 + 2 * t + j;
-            q.pos[nt][j] = cc < nc ? pos0 + (c0 + cc) / G : -1;
-        }
-    }
-}
 
 template <int NT>
 __device__ __forceinline__ void reset(Elem<NT>& e) {
@@ -353,7 +303,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                 ps = col_max(ps);
                 if (ps * e.c[nt][j] > kTopW * pow2(-20) && ps < INFINITY) {
                     const float c = pow2(max(-126, min(100, 6 - 20 - exponent(ps))));
-                    al *= c * (1.f / e.c[nt][j]);  // powers of two: exact, or 0
+                    al *= c * inv_pow2(e.c[nt][j]);  // powers of two: exact, or 0
                     e.c[nt][j] = c;
                 }
                 if (!first) {
@@ -431,13 +381,13 @@ __device__ __forceinline__ void hand_arrive(int quarter) {
 }
 __device__ __forceinline__ void hand_wait(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(quarter) : "memory"); }
 
-// The two blocks of a step from global to shared memory, by one warp.
-__device__ __forceinline__ void copy_step(char* dst, const char* src) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < kStepBytes / 512; ++j)
-        wm::cp_async16_zfill(dst + (j * 32 + lane) * 16, src + (j * 32 + lane) * 16, true);
-    static_assert(kStepBytes % 512 == 0, "whole rounds of 32 lanes");
+// The two blocks of a step from global to shared memory, asked for by one lane.
+__device__ __forceinline__ void ask_step(char* dst, const char* src, uint64_t* full) {
+    mbar_arrive_expect_tx(full, kStepBytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(kStepBytes), "r"(smem_u32(full))
+                 : "memory");
 }
 
 // An element's end, in place: l and the zeros' sums over the column's lanes (za[j][0]
@@ -451,7 +401,7 @@ __device__ __forceinline__ void finish(Elem<NT>& e) {
         for (int j = 0; j < 2; ++j) {
             e.l[nt][j] = col_sum(e.l[nt][j]);
             const float z[2] = {col_sum(e.za[nt][j][0]), col_sum(e.za[nt][j][1])};
-            const float inv = 1.f / e.c[nt][j];  // a power of two up to 2^126
+            const float inv = inv_pow2(e.c[nt][j]);
 #pragma unroll
             for (int d = 0; d < 8; d += 2)
 #pragma unroll
@@ -524,24 +474,76 @@ __device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u
     return ((size_t)x.id * a.max_units + u) * NT;
 }
 
+// The queries of a set: asked for (ask_query) before the keys, which they would
+// otherwise wait behind, and made operands (load_query) when they are there.  Lane
+// (g, t) holds column g's dims of its words of a key's row: 16t..16t+15 and 64+16t..64+16t+15.
+template <int NT>
+struct RawQuery {
+    uint4 w[NT][4];
+};
+template <int NT>
+__device__ __forceinline__ void ask_query(RawQuery<NT>& r, const AttnArgs& a, const Set& x, int G) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = x.c0 + nt * 8 + g;
+        const bool in = nt * 8 + g < x.nc;
+        const bf16* q = a.q + (in ? (long)(x.r0 + c / G) * a.ldq + (x.h * G + c % G) * kHeadDim : 0) + 16 * t;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            r.w[nt][w] = in ? *reinterpret_cast<const uint4*>(q + (w & 1) * 64 + (w >> 1) * 8) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// q' by the power of two that its largest number asks for; the groups' sums by the
+// tensor cores from the same operands (ones, and 16 for the codes' high halves).
+template <int NT>
+__device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, const Set& x, int G) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        uint32_t top = 0;  // of the absolute values' bits
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint4 v = r.w[nt][w];
+            top = __vimax3_u16x2(top, v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+            top = __vimax3_u16x2(top, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+        }
+        uint32_t m = max(top & 0xffffu, top >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = max(-100, min(126, 13 - ((int)(m >> 7) - 127)));
+        const float up = pow2(e), up4 = pow2(e - 4);
+        float sum[2][4];
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) sum[gr][0] = sum[gr][1] = sum[gr][2] = sum[gr][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint4 v = r.w[nt][w];
+            q.b[nt][2 * w][0] = pack_half(lo_f(v.x) * up, lo_f(v.z) * up);
+            q.b[nt][2 * w][1] = pack_half(lo_f(v.y) * up, lo_f(v.w) * up);
+            q.b[nt][2 * w + 1][0] = pack_half(hi_f(v.x) * up4, hi_f(v.z) * up4);
+            q.b[nt][2 * w + 1][1] = pack_half(hi_f(v.y) * up4, hi_f(v.w) * up4);
+            mma_f16(sum[w & 1], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
+            mma_f16(sum[w & 1], 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, q.b[nt][2 * w + 1][0],
+                    q.b[nt][2 * w + 1][1]);
+        }
+        const float f = pow2(24 - e) * kLog2eOverSqrtD;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            q.F[nt][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
+            q.Q0[nt][j] = sum[0][j] * (q.F[nt][j] * pow2(-24));
+            q.Q1[nt][j] = sum[1][j] * (q.F[nt][j] * pow2(-24));
+            const int cc = nt * 8 + 2 * t + j;
+            q.pos[nt][j] = cc < x.nc ? x.pos0 + (x.c0 + cc) / G : -1;
+        }
+    }
+}
+
 // The output row of a set's column, nullptr past the last.
 __device__ __forceinline__ bf16* out_row(const AttnArgs& a, const Set& x, int G, int col) {
     const int c = x.c0 + col;
     return col < x.nc ? a.out + (long)(x.r0 + c / G) * a.ldo + (x.h * G + c % G) * kHeadDim : nullptr;
-}
-
-// Step i of the kElemSteps that a warp asked for, one after the other, is there.
-__device__ __forceinline__ void wait_step(int i) {
-    static_assert(kElemSteps == 4, "one case each");
-    if (i == 0)
-        wm::cp_async_wait<3>();
-    else if (i == 1)
-        wm::cp_async_wait<2>();
-    else if (i == 2)
-        wm::cp_async_wait<1>();
-    else
-        wm::cp_async_wait<0>();
-    __syncwarp();
 }
 
 // A unit's partial (one tile of columns): O by the caller's lanes, M and L by lanes 0..3.
@@ -559,11 +561,13 @@ struct Wide {
     static constexpr int kBuf = kElemSteps * kStepBytes;                          // a warp's keys, then its output
     static constexpr int kBytes = kWideWarps * kBuf + kWideWarps * NT * 4 * 32 * 4;  // and its maxima and sums
 };
+static_assert(kWideWarps * kElemSteps * 8 <= 64, "barriers");
 static_assert(Wide<2>::kBuf >= 2 * 4096, "a warp's output fits its buffer");
 
 template <int NT>
 __global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 8 : 4) wide_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
+    __shared__ uint64_t full[kWideWarps][kElemSteps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group;
     Set x;
@@ -574,21 +578,25 @@ __global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 8 : 4) wide_kernel(
     char* buf = smem + warp * Wide<NT>::kBuf;
     Query<NT> q;
     Elem<NT> e;
+    RawQuery<NT> raw;
     pdl_wait();
     pdl_trigger();
-    if (steps) {
+    ask_query(raw, a, x, G);
+    if (steps && lane == 0) {
         const char* src = tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h);
-#pragma unroll
-        for (int i = 0; i < kElemSteps; ++i) {
-            if (i < steps) copy_step(buf + i * kStepBytes, src + i * kStepBytes);
-            wm::cp_async_commit();
-        }
+        for (int i = 0; i < steps; ++i) mbar_init(&full[warp][i], 1);
+        mbar_init_fence();
+        for (int i = 0; i < steps; ++i) ask_step(buf + i * kStepBytes, src + i * kStepBytes, &full[warp][i]);
     }
-    load_query(q, a, x.r0, G, x.h, x.c0, x.nc, x.pos0);
+    __syncwarp();
+    load_query(q, raw, x, G);
     reset(e);
+    bool there = true;  // until a wait gives up, which status then says; every copy is waited for
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-        wait_step(i);
+        const bool ok = mbar_wait(&full[warp][i], 0, a.status);
+        there = __all_sync(0xffffffffu, there && ok);
+        if (!there) continue;
         any_step(e, q, buf + i * kStepBytes, k0 + i * kStepKeys, p_first, i == 0);
     }
     // ---- join the two elements: every warp puts its own down and takes half the tiles of both ----
@@ -643,10 +651,11 @@ struct Fetch {
     const int* table;
     int left;                  // steps of the element not yet fetched
     int elem, u, last;         // the element (2 x unit + half), its unit in the set, the set's last position
+    uint64_t full[kDeepStages];
 };
-constexpr int kDeepBuf = kDeepStages * kStepBytes + 64;  // a warp's ring, Fetch
+constexpr int kDeepBuf = kDeepStages * kStepBytes + 128;  // a warp's ring, Fetch
 static_assert(kDeepUnits >= 2, "no empty quarter");
-static_assert(sizeof(Fetch) <= 64, "Fetch");
+static_assert(sizeof(Fetch) <= 128, "Fetch");
 constexpr int kHandFloats = 1024 + 128;                  // an element handed over: output, maxima and sums
 constexpr int kDeepBytes = kDeepWarps * (kDeepBuf + kHandFloats * 4);
 
@@ -670,22 +679,29 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
     float* hand = reinterpret_cast<float*>(smem + kDeepWarps * kDeepBuf);  // [quarter][kHandFloats]
     Set x;
     int u = find<1>(a, G, v >> 1, x);
-    // The fetching side, up to kDeepStages steps ahead, in shared memory (registers are what this kernel lacks).
+    RawQuery<1> raw;
+    ask_query(raw, a, x, G);
+    // The fetching side: lane 0, up to kDeepStages steps ahead, its state in shared memory (registers are what this
+    // kernel lacks) but for the next element's page, which is asked for an element ahead.
     Fetch* f = reinterpret_cast<Fetch*>(buf + kDeepStages * kStepBytes);
-    auto open_set = [&](const Set& y, int unit) {  // lane 0
+    int ahead = 0;
+    auto open_set = [&](const Set& y, int unit, int half) {
         const View& kv = a.rows.kv[y.s];
         f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
         f->table = kv.table;
         f->last = y.pos0 + (y.nc - 1) / G;
         f->u = unit;
+        const int page = unit * kElems + half;
+        if (page * kElemKeys <= f->last) ahead = __ldg(kv.table + page);
     };
-    auto open = [&](int elem) {  // lane 0
-        const int k = f->u * kUnit + (elem & 1) * kElemKeys, keys = f->last + 1 - k;
+    auto open = [&](int elem) {
+        const int page = f->u * kElems + (elem & 1), keys = f->last + 1 - page * kElemKeys;
         f->elem = elem;
         f->left = keys <= 0 ? 0 : min(kElemSteps, (keys + kStepKeys - 1) / kStepKeys);
-        if (keys > 0) f->next = f->heads + (size_t)__ldg(f->table + k / kPage) * n_kv * kTileBytes;
+        f->next = f->heads + (size_t)ahead * n_kv * kTileBytes;
+        if (keys > kElemKeys) ahead = __ldg(f->table + page + 1);
     };
-    auto open_next = [&]() {  // lane 0: the element after f->elem that has keys (a set's last unit may lack a second)
+    auto open_next = [&]() {  // the element after f->elem that has keys (a set's last unit may lack a second)
         while (f->left == 0 && f->elem + 1 < end) {
             const int elem = f->elem + 1;
             if ((elem & 1) == 0) {
@@ -694,36 +710,36 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
                 } else {
                     Set y;
                     const int w = find<1>(a, G, elem >> 1, y);
-                    open_set(y, w);
+                    open_set(y, w, 0);
                 }
             }
             open(elem);
         }
     };
+    int fslot = 0;
+    auto fetch = [&]() {
+        if (lane == 0 && f->left > 0) {
+            ask_step(buf + fslot * kStepBytes, f->next, &f->full[fslot]);
+            f->next += kStepBytes;
+            --f->left;
+            open_next();
+        }
+        if (++fslot == kDeepStages) fslot = 0;
+    };
     if (lane == 0) {
-        open_set(x, u);
+        for (int k = 0; k < kDeepStages; ++k) mbar_init(&f->full[k], 1);
+        mbar_init_fence();
+        open_set(x, u, v & 1);
         open(v);
         open_next();
     }
     __syncwarp();
-    int fslot = 0;
-    auto fetch = [&]() {
-        if (f->left > 0) {
-            copy_step(buf + fslot * kStepBytes, f->next);
-            __syncwarp();
-            if (lane == 0) {
-                f->next += kStepBytes;
-                --f->left;
-                open_next();
-            }
-            __syncwarp();
-        }
-        wm::cp_async_commit();
-        if (++fslot == kDeepStages) fslot = 0;
-    };
-    fetch();  // one step on its way before the queries, which would wait behind more
-    bool fresh = true;  // the set's queries are to be loaded
+#pragma unroll 1
+    for (int k = 0; k < kDeepStages; ++k) fetch();
+    bool fresh = true;  // the set's queries are to be made operands
     int slot = 0;
+    uint32_t phase = 0;
+    bool there = true;  // until a wait gives up, which status then says
     Query<1> q;
     Elem<1> e;
     float4 O[8];      // a unit's first element, until its second is there
@@ -731,23 +747,22 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
     bool held = false;
 #pragma unroll 1
     while (true) {
-        if (fresh) load_query(q, a, x.r0, G, x.h, 0, x.nc, x.pos0);
-        if (fresh && slot == 0 && fslot == 1) {
-#pragma unroll 1
-            for (int k = 1; k < kDeepStages; ++k) fetch();
-        }
+        if (fresh) load_query(q, raw, x, G);
         fresh = false;
         const int p_first = x.pos0, p_last = x.pos0 + (x.nc - 1) / G;
         const int k0 = u * kUnit + (v & 1) * kElemKeys, k1 = min(k0 + kElemKeys, p_last + 1);
         reset(e);
 #pragma unroll 1
         for (int k = k0; k < k1; k += kStepKeys) {
-            wm::cp_async_wait<kDeepStages - 1>();
-            __syncwarp();
+            there = there && __all_sync(0xffffffffu, mbar_wait(&f->full[slot], phase, a.status));
+            if (!there) continue;  // nothing more is asked for
             any_step(e, q, buf + slot * kStepBytes, k, p_first, k == k0);
             __syncwarp();  // the stage has been read
             fetch();
-            if (++slot == kDeepStages) slot = 0;
+            if (++slot == kDeepStages) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
         finish(e);
         const bool second = v & 1, ends = v + 1 == end;
@@ -810,11 +825,19 @@ __global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const 
                 ++u;
             } else {
                 u = find<1>(a, G, v >> 1, x);
+                ask_query(raw, a, x, G);
                 fresh = true;
             }
         }
     }
-    wm::cp_async_wait_all();
+    if (!there)  // the copies of the other stages end before the CTA does, or these waits run out too
+        for (int k = 1; k < kDeepStages; ++k) {
+            if (++slot == kDeepStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+            mbar_wait(&f->full[slot], phase, a.status);
+        }
 }
 
 // Joins n <= kFan partials of one tile in order, by one warp.  Partial i's eight maxima

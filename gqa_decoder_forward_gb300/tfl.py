@@ -119,6 +119,7 @@ SIGNATURES = {
     "tfl_kv4_attn_bytes": (ctypes.c_size_t, [ctypes.c_int] * 5),
     "tfl_kv4_attn_init": (ctypes.c_int, [ctypes.c_int] * 5 + [_vp, ctypes.c_size_t, ctypes.POINTER(_vp)]),
     "tfl_kv4_attn_free": (None, [_vp]),
+    "tfl_kv4_attn_status": (ctypes.c_int, [_vp, _vp]),
     "tfl_kv4_attention": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp,
                                          ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
     "tfl_kv4_step_workspace_bytes": (ctypes.c_size_t, [_vp]),
@@ -557,6 +558,10 @@ class KV4Attention:
         if getattr(self, "handle", None):
             lib().tfl_kv4_attn_free(self.handle)
             self.handle = None
+
+
+def tfl_kv4_attn_status(attn: KV4Attention, stream=None) -> int:
+    return int(lib().tfl_kv4_attn_status(attn.handle, _stream(stream)))
 
 
 def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:

@@ -552,6 +552,10 @@ size_t tfl_kv4_attn_bytes(int n_q, int n_kv, int head_dim, int max_rows, int max
 int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_positions, void* workspace,
                       size_t ws_bytes, tfl_kv4_attn** out);
 void tfl_kv4_attn_free(tfl_kv4_attn* attn);
+/* Synchronises `stream`, reads and clears the object's status word: TFL_OK, or
+ * TFL_E_DEVICE if a kernel of tfl_kv4_attention gave up a bounded wait (its rows are
+ * then undefined).  tfl_decode_step_kv4 reports through tfl_status. */
+int tfl_kv4_attn_status(tfl_kv4_attn* attn, void* stream);
 int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, void* stream);
 

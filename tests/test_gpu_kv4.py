@@ -194,6 +194,7 @@ def attend(attn, kvs, pos0, rows, q, layer=0, stream=None):
     out = torch.full((n + 1, q.shape[1] * 128), 3.0, dtype=torch.bfloat16, device="cuda")
     tfl.tfl_kv4_attention(attn, tfl.KV4Rows(kvs, pos0, rows), layer, cuda_bf16(q).view(-1, q.shape[1] * 128), out, stream)
     got = host_f32(out)
+    assert tfl.tfl_kv4_attn_status(attn) == tfl.TFL_OK
     assert (got[n] == 3.0).all()
     return got[:n].reshape(n, q.shape[1], 128)
 

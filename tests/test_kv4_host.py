@@ -73,6 +73,7 @@ def test_null_objects_are_refused(L):
     assert L.tfl_kv4_write(kvs, 17, 0, one, one, 256, 512, 128, None) == tfl.TFL_E_ARG
     assert L.tfl_kv4_write(kvs, 0, 0, one, one, 256, 512, 128, None) == tfl.TFL_E_ARG
     assert L.tfl_kv4_attention(None, kvs, 1, 0, one, one, 256, 1024, 512, 1024, None) == tfl.TFL_E_ARG
+    assert L.tfl_kv4_attn_status(None, None) == tfl.TFL_E_ARG
     assert L.tfl_kv4_reset(None, 0) == tfl.TFL_E_ARG
     assert L.tfl_kv4_length(None) == -1 and L.tfl_kv4_capacity(None) == -1
     L.tfl_kv4_free(None)
