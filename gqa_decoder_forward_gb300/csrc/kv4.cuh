@@ -110,6 +110,8 @@ struct AttnArgs {
     int max_units;
     int* status;         // device status word: a bounded wait that gives up raises kStatusDevice
     int group;           // set by launch_attn: query heads per KV head,
+    int group_inv;       // 65536 / group, rounded up,
+    int per_sm, direct;  // CTAs of an SM; every stream has one unit, whose warp writes the output,
     int item_start[kMaxStreams + 1]; // first unit (over its sets) of a stream,
     int set_start[kMaxStreams];       // and its first set of columns
 };

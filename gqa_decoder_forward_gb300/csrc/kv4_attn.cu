@@ -23,17 +23,13 @@
 // of the largest.  Likewise m moves only when an x_t passes it by 8.  Both decisions
 // are a column's own, so a column's bits do not depend on its neighbours.
 //
-// Split.  An element is 128 keys at absolute positions, taken by one warp in four
-// steps of 32 with a fresh (m, l, c, output); a unit is two elements (256 keys),
-// folded in order of position.  A second kernel joins the units: groups of 16, then
-// the groups, in order.  So the bits depend on the position alone, while the units
-// are spread in one of two ways (launch_attn):
-//   wide   a unit per CTA, an element per warp: short caches, where a
-//          call's time is one CTA's latency;
-//   deep   a persistent grid whose warps take equal shares of the units, keys and
-//          values through a ring of the warp's own, without any barrier: many units.
-// A warp's keys come by bulk copies that one of its lanes asks for, into shared memory
-// that no other warp reads.
+// Split.  A unit is 256 keys of a KV head at absolute positions, taken by one warp in
+// steps of 32 with a fresh (m, l, c, output).  A second kernel joins the units: groups
+// of 16, then the groups, in order.  So the bits depend on the position alone, however
+// the units are spread: the grid is persistent, each warp takes an equal share of the
+// call's units one after the other, and meets no other warp.  A warp's keys come by
+// bulk copies that one of its lanes asks for, into shared memory that no other warp
+// reads, always kStages - 1 steps ahead.
 #include <cfloat>
 #include <cuda_fp16.h>
 
@@ -47,19 +43,17 @@ namespace {
 
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
-constexpr int kElemKeys = kPage;                   // keys of an element: a page
-constexpr int kElemSteps = kElemKeys / kStepKeys;  // 4
-constexpr int kElems = 2;                          // elements of a unit
-constexpr int kUnit = kElems * kElemKeys;          // 256 keys
-constexpr int kWideWarps = kElems;
-constexpr int kDeepWarps = 4;
-constexpr int kDeepCtas = 3;                       // CTAs of an SM
-constexpr int kDeepStages = 3;                     // steps of a deep warp's ring
+constexpr int kUnit = 256;                         // keys of a unit
+constexpr int kWarps = 4;                          // of a CTA
+#ifndef DC
+#define DC 4
+#define DS 3
+#endif
+constexpr int kCtas1 = DC, kStages1 = DS;          // CTAs of an SM and steps of a warp's ring, one tile of columns
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
 constexpr int kMaxJoinBytes = ((1 << 20) / kUnit + kFan - 1) / kFan * kGroupBytes;
-constexpr int kDeepUnits = 4;                  // units of a CTA from which a call's units go to the persistent grid
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
@@ -148,13 +142,13 @@ struct Query {
 };
 
 template <int NT>
-struct Elem {
+struct State {
     float m[NT][2], l[NT][2], c[NT][2], za[NT][2][2];  // l and za: this lane's keys only
     float o[NT][8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
 };
 
 template <int NT>
-__device__ __forceinline__ void reset(Elem<NT>& e) {
+__device__ __forceinline__ void reset(State<NT>& e) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -171,10 +165,10 @@ __device__ __forceinline__ void reset(Elem<NT>& e) {
 
 // The 32 keys from position k0, whose two blocks are at buf.  EDGE: some column does
 // not see all of them; what it does not see takes no part, whatever its bytes.
-// first: the element's first step.  (A body of its own for that costs more in
+// first: the unit's first step.  (A body of its own for that costs more in
 // instruction cache misses than its tests.)
 template <int NT, bool EDGE>
-__device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, bool first) {
+__device__ __forceinline__ void step(State<NT>& e, const Query<NT>& q, const char* buf, int k0, bool first) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int krow = key_of_row(g);  // rows g and g + 8 of the tiles: keys krow, krow + 8
     const int k_at = krow * kRowBytes + ((t ^ (krow & 2)) << 4);
@@ -274,7 +268,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                                                (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
         }
         // A score passes m by more than 8, or a w passes 2^15: m, c and the running sums move in the
-        // columns where it does.  An element's first step sets them.
+        // columns where it does.  A unit's first step sets them.
         if (move) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -302,7 +296,7 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
                     }
                 ps = col_max(ps);
                 if (ps * e.c[nt][j] > kTopW * pow2(-20) && ps < INFINITY) {
-                    const float c = pow2(max(-126, min(100, 6 - 20 - exponent(ps))));
+                    const float c = pow2(max(-100, min(100, 6 - 20 - exponent(ps))));
                     al *= c * inv_pow2(e.c[nt][j]);  // powers of two: exact, or 0
                     e.c[nt][j] = c;
                 }
@@ -367,20 +361,6 @@ __device__ __forceinline__ void step(Elem<NT>& e, const Query<NT>& q, const char
     }
 }
 
-template <int NT>
-__device__ __forceinline__ void any_step(Elem<NT>& e, const Query<NT>& q, const char* buf, int k0, int p_first, bool first) {
-    if (k0 + kStepKeys - 1 > p_first)
-        step<NT, true>(e, q, buf, k0, first);
-    else
-        step<NT, false>(e, q, buf, k0, first);
-}
-
-// Hand-over of an element to the warp of the quarter before: hardware barriers of the two warps.
-__device__ __forceinline__ void hand_arrive(int quarter) {
-    asm volatile("bar.arrive %0, 64;" ::"r"(quarter) : "memory");
-}
-__device__ __forceinline__ void hand_wait(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(quarter) : "memory"); }
-
 // The two blocks of a step from global to shared memory, asked for by one lane.
 __device__ __forceinline__ void ask_step(char* dst, const char* src, uint64_t* full) {
     mbar_arrive_expect_tx(full, kStepBytes);
@@ -390,57 +370,37 @@ __device__ __forceinline__ void ask_step(char* dst, const char* src, uint64_t* f
                  : "memory");
 }
 
-// An element's end, in place: l and the zeros' sums over the column's lanes (za[j][0]
-// becomes l's), o from code units and c to the output's own scale, zeros added.  Of the
-// pairs of tiles, the whole bytes less the low codes leave the high ones.
+// A unit's end, in place: l over the column's lanes, o from code units and c to the
+// output's own scale, the zeros' sums added.  Of the pairs of tiles, the whole bytes
+// less the low codes leave the high ones.
 template <int NT>
-__device__ __forceinline__ void finish(Elem<NT>& e) {
+__device__ __forceinline__ void finish(State<NT>& e) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             e.l[nt][j] = col_sum(e.l[nt][j]);
             const float z[2] = {col_sum(e.za[nt][j][0]), col_sum(e.za[nt][j][1])};
-            const float inv = inv_pow2(e.c[nt][j]);
+            const float inv = inv_pow2(e.c[nt][j]), lo = inv * kLoCode, hi = inv * kHiCode;  // c >= 2^-100
 #pragma unroll
             for (int d = 0; d < 8; d += 2)
 #pragma unroll
                 for (int k = j; k < 4; k += 2) {
-                    const float lo = e.o[nt][d][k], hi = e.o[nt][d + 1][k] - lo;
-                    e.o[nt][d][k] = fmaf(lo * kLoCode, inv, z[d >> 2]);
-                    e.o[nt][d + 1][k] = fmaf(hi * kHiCode, inv, z[d >> 2]);
+                    e.o[nt][d + 1][k] = fmaf(e.o[nt][d + 1][k] - e.o[nt][d][k], hi, z[d >> 2]);
+                    e.o[nt][d][k] = fmaf(e.o[nt][d][k], lo, z[d >> 2]);
                 }
         }
 }
 
-// Joins two finished partials of a column; (kUnset, 0, 0) changes nothing.
-__device__ __forceinline__ void join_weights(float& m0, float m1, float& l0, float l1, float& w0, float& w1) {
-    const float m = fmaxf(m0, m1);
-    w0 = ex2(m0 - m);
-    w1 = ex2(m1 - m);
-    l0 = fmaf(l1, w1, l0 * w0);
-    m0 = m;
-}
-__device__ __forceinline__ float4 join4(float4 a, float4 b, const float (&w0)[2], const float (&w1)[2]) {
-    return make_float4(fmaf(b.x, w1[0], a.x * w0[0]), fmaf(b.y, w1[1], a.y * w0[1]), fmaf(b.z, w1[0], a.z * w0[0]),
-                       fmaf(b.w, w1[1], a.w * w0[1]));
-}
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
 __device__ __forceinline__ float4 f4(const float (&o)[4]) { return make_float4(o[0], o[1], o[2], o[3]); }
 
-// Tile d's part of the output: its columns' rows of dims, columns past nc left out.
-template <class Row>
-__device__ __forceinline__ void put_out(int d, float4 O, const float (&L)[2], Row row) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int dim = 64 * (d >> 2) + 8 * g + (d & 3);
-    if (bf16* o = row(2 * t)) {
-        o[dim] = rn(O.x / L[0]);
-        o[dim + 4] = rn(O.z / L[0]);
-    }
-    if (bf16* o = row(2 * t + 1)) {
-        o[dim] = rn(O.y / L[1]);
-        o[dim + 4] = rn(O.w / L[1]);
-    }
-}
+// c / (query heads per KV head), c below 4,096.
+__device__ __forceinline__ int row_of(const AttnArgs& a, int c) { return (c * a.group_inv) >> 16; }
 
 // What a (stream, KV head, columns) set of a call is.
 struct Set {
@@ -488,7 +448,7 @@ __device__ __forceinline__ void ask_query(RawQuery<NT>& r, const AttnArgs& a, co
     for (int nt = 0; nt < NT; ++nt) {
         const int c = x.c0 + nt * 8 + g;
         const bool in = nt * 8 + g < x.nc;
-        const bf16* q = a.q + (in ? (long)(x.r0 + c / G) * a.ldq + (x.h * G + c % G) * kHeadDim : 0) + 16 * t;
+        const bf16* q = a.q + (in ? (long)(x.r0 + row_of(a, c)) * a.ldq + (x.h * G + c - row_of(a, c) * G) * kHeadDim : 0) + 16 * t;
 #pragma unroll
         for (int w = 0; w < 4; ++w)
             r.w[nt][w] = in ? *reinterpret_cast<const uint4*>(q + (w & 1) * 64 + (w >> 1) * 8) : make_uint4(0, 0, 0, 0);
@@ -498,7 +458,7 @@ __device__ __forceinline__ void ask_query(RawQuery<NT>& r, const AttnArgs& a, co
 // q' by the power of two that its largest number asks for; the groups' sums by the
 // tensor cores from the same operands (ones, and 16 for the codes' high halves).
 template <int NT>
-__device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, const Set& x, int G) {
+__device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, const AttnArgs& a, const Set& x) {
     const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -535,308 +495,188 @@ __device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, 
             q.Q0[nt][j] = sum[0][j] * (q.F[nt][j] * pow2(-24));
             q.Q1[nt][j] = sum[1][j] * (q.F[nt][j] * pow2(-24));
             const int cc = nt * 8 + 2 * t + j;
-            q.pos[nt][j] = cc < x.nc ? x.pos0 + (x.c0 + cc) / G : -1;
+            q.pos[nt][j] = cc < x.nc ? x.pos0 + row_of(a, x.c0 + cc) : -1;
         }
     }
 }
 
-// The output row of a set's column, nullptr past the last.
-__device__ __forceinline__ bf16* out_row(const AttnArgs& a, const Set& x, int G, int col) {
-    const int c = x.c0 + col;
-    return col < x.nc ? a.out + (long)(x.r0 + c / G) * a.ldo + (x.h * G + c % G) * kHeadDim : nullptr;
-}
-
-// A unit's partial (one tile of columns): O by the caller's lanes, M and L by lanes 0..3.
-__device__ __forceinline__ void put_max_sum(const AttnArgs& a, size_t at, const float (&M)[2], const float (&L)[2]) {
-    const int lane = threadIdx.x & 31;
-    if (lane < 4) {
-        *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * lane) = make_float2(M[0], M[1]);
-        *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(L[0], L[1]);
-    }
-}
-
-// Wide: a unit per CTA, an element per warp.
-template <int NT>
-struct Wide {
-    static constexpr int kBuf = kElemSteps * kStepBytes;                          // a warp's keys, then its output
-    static constexpr int kBytes = kWideWarps * kBuf + kWideWarps * NT * 4 * 32 * 4;  // and its maxima and sums
+// Rows of the output of this lane's two columns of a tile (nullptr past the last column).
+struct OutRows {
+    bf16* r[2];
 };
-static_assert(kWideWarps * kElemSteps * 8 <= 64, "barriers");
-static_assert(Wide<2>::kBuf >= 2 * 4096, "a warp's output fits its buffer");
-
-template <int NT>
-__global__ void __launch_bounds__(kWideWarps * 32, NT == 1 ? 8 : 4) wide_kernel(const __grid_constant__ AttnArgs a) {
-    extern __shared__ __align__(128) char smem[];
-    __shared__ uint64_t full[kWideWarps][kElemSteps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.group;
-    Set x;
-    const int u = find<NT>(a, G, blockIdx.x, x);
-    const int p_first = x.pos0 + x.c0 / G, p_last = x.pos0 + (x.c0 + x.nc - 1) / G;
-    const int k0 = u * kUnit + warp * kElemKeys;
-    const int steps = k0 > p_last ? 0 : min(kElemSteps, (p_last - k0) / kStepKeys + 1);
-    char* buf = smem + warp * Wide<NT>::kBuf;
-    Query<NT> q;
-    Elem<NT> e;
-    RawQuery<NT> raw;
-    pdl_wait();
-    pdl_trigger();
-    ask_query(raw, a, x, G);
-    if (steps && lane == 0) {
-        const char* src = tile(a.rows.kv[x.s], a.rows.layer, a.rows.n_kv, k0, x.h);
-        for (int i = 0; i < steps; ++i) mbar_init(&full[warp][i], 1);
-        mbar_init_fence();
-        for (int i = 0; i < steps; ++i) ask_step(buf + i * kStepBytes, src + i * kStepBytes, &full[warp][i]);
+__device__ __forceinline__ OutRows out_rows(const AttnArgs& a, const Set& x, int G, int nt) {
+    OutRows o;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int col = nt * 8 + 2 * (threadIdx.x & 3) + j, c = x.c0 + col, row = row_of(a, c);
+        o.r[j] = col < x.nc ? a.out + (long)(x.r0 + row) * a.ldo + (x.h * G + c - row * G) * kHeadDim : nullptr;
     }
-    __syncwarp();
-    load_query(q, raw, x, G);
-    reset(e);
-    bool there = true;  // until a wait gives up, which status then says; every copy is waited for
-#pragma unroll 1
-    for (int i = 0; i < steps; ++i) {
-        const bool ok = mbar_wait(&full[warp][i], 0, a.status);
-        there = __all_sync(0xffffffffu, there && ok);
-        if (!there) continue;
-        any_step(e, q, buf + i * kStepBytes, k0 + i * kStepKeys, p_first, i == 0);
+    return o;
+}
+// Tile d of them, from its output and the columns' 1 / l.
+__device__ __forceinline__ void put_out(const OutRows& o, int d, float4 O, const float (&R)[2]) {
+    const int dim = 64 * (d >> 2) + 8 * ((threadIdx.x & 31) >> 2) + (d & 3);
+    if (o.r[0]) {
+        o.r[0][dim] = rn(O.x * R[0]);
+        o.r[0][dim + 4] = rn(O.z * R[0]);
     }
-    // ---- join the two elements: every warp puts its own down and takes half the tiles of both ----
-    __syncwarp();  // the warp has read its keys
-    finish(e);
-    float* sc = reinterpret_cast<float*>(smem + kWideWarps * Wide<NT>::kBuf);  // [element][tile][m, l][lane]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float4* o = reinterpret_cast<float4*>(buf) + nt * 256 + lane;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[d * 32] = f4(e.o[nt][d]);
-        float* y = sc + (warp * NT + nt) * 128 + lane;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            y[j * 32] = e.m[nt][j];
-            y[(2 + j) * 32] = e.l[nt][j];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const float *y0 = sc + nt * 128 + lane, *y1 = y0 + NT * 128;
-        float M[2], L[2], w0[2], w1[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            M[j] = y0[j * 32];
-            L[j] = y0[(2 + j) * 32];
-            join_weights(M[j], y1[j * 32], L[j], y1[(2 + j) * 32], w0[j], w1[j]);
-        }
-        const size_t at = partial<NT>(a, x, u) + nt;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int d = warp * 4 + k;
-            const float4* o = reinterpret_cast<const float4*>(smem) + nt * 256 + d * 32 + lane;
-            const float4 O = join4(o[0], o[Wide<NT>::kBuf / 16], w0, w1);
-            if (x.nu == 1)
-                put_out(d, O, L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
-            else
-                reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O;
-        }
-        if (x.nu > 1 && warp == 0) put_max_sum(a, at, M, L);
+    if (o.r[1]) {
+        o.r[1][dim] = rn(O.y * R[1]);
+        o.r[1][dim + 4] = rn(O.w * R[1]);
     }
 }
 
-// Deep: a persistent grid.  A CTA takes an equal share of the call's units, its warps equal
-// shares of their elements, one element after the other with the next steps' keys always
-// on their way.  A unit whose elements fall to two warps is joined by the warp of the
-// first, at its end; the warp of the second has left its part in shared memory at its own
-// beginning, so nobody waits in practice.
+// The fetching side of a warp: lane 0, its state in shared memory.
 struct Fetch {
     const char *next, *heads;  // the step to fetch; tile 0 of the layer and head
     const int* table;
-    int left;                  // steps of the element not yet fetched
-    int elem, u, last;         // the element (2 x unit + half), its unit in the set, the set's last position
-    uint64_t full[kDeepStages];
+    int item, left;            // the unit, its steps not yet fetched
+    int u, last;               // its number in the set, the set's last position
+    int page;                  // the unit's second page
 };
-constexpr int kDeepBuf = kDeepStages * kStepBytes + 128;  // a warp's ring, Fetch
-static_assert(kDeepUnits >= 2, "no empty quarter");
-static_assert(sizeof(Fetch) <= 128, "Fetch");
-constexpr int kHandFloats = 1024 + 128;                  // an element handed over: output, maxima and sums
-constexpr int kDeepBytes = kDeepWarps * (kDeepBuf + kHandFloats * 4);
 
-__global__ void __launch_bounds__(kDeepWarps * 32, kDeepCtas) deep_kernel(const __grid_constant__ AttnArgs a) {
+template <int NT>
+struct Cfg {
+    static constexpr int kCtas = NT == 1 ? kCtas1 : 2;      // of an SM
+    static constexpr int kStages = NT == 1 ? kStages1 : 5;    // steps of a warp's ring
+    static constexpr int kBuf = kStages * (kStepBytes + 8) + 64;
+    static constexpr int kBufBytes = (kBuf + 127) / 128 * 128;
+    static constexpr int kBytes = kWarps * kBufBytes;
+};
+static_assert(sizeof(Fetch) <= 64, "Fetch");
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kStages = Cfg<NT>::kStages;
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_kv = a.rows.n_kv, G = a.group;
-    // units of this CTA, elements of this warp; warps take the CTA's quarters in turn from CTA to CTA, so
-    // that a scheduler (the same warp of an SM's CTAs) gets every quarter
+    // a full grid: the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
+    // neighbouring shares, so that their sum differs by at most one unit between schedulers
     const int items = a.item_start[a.rows.n_streams];
-    const int first = (int)((long)blockIdx.x * items / gridDim.x), last = (int)((long)(blockIdx.x + 1) * items / gridDim.x);
-    const int sms = gridDim.x / kDeepCtas, quarter = (warp + blockIdx.x / sms) % kDeepWarps, n = 2 * (last - first);
-    int v = 2 * first + quarter * n / kDeepWarps;
-    const int end = 2 * first + (quarter + 1) * n / kDeepWarps;
+    const int per = a.per_sm, sms = gridDim.x / per;
+    const long share = ((long)(blockIdx.x % sms) * kWarps + warp) * per + blockIdx.x / sms, shares = (long)gridDim.x * kWarps;
+    int i = (int)(share * items / shares);
+    const int end = (int)((share + 1) * items / shares);
     pdl_wait();
     pdl_trigger();
-    // A CTA has at least two units (launch_attn), so no quarter is empty, and the quarter after one that ends
-    // with a unit's first element begins with its second.
+    if (i >= end) return;
 
-    char* buf = smem + warp * kDeepBuf;
-    float* hand = reinterpret_cast<float*>(smem + kDeepWarps * kDeepBuf);  // [quarter][kHandFloats]
+    char* buf = smem + warp * Cfg<NT>::kBufBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
+    Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
     Set x;
-    int u = find<1>(a, G, v >> 1, x);
-    RawQuery<1> raw;
-    ask_query(raw, a, x, G);
-    // The fetching side: lane 0, up to kDeepStages steps ahead, its state in shared memory (registers are what this
-    // kernel lacks) but for the next element's page, which is asked for an element ahead.
-    Fetch* f = reinterpret_cast<Fetch*>(buf + kDeepStages * kStepBytes);
-    int ahead = 0;
-    auto open_set = [&](const Set& y, int unit, int half) {
+    int u = find<NT>(a, G, i, x);
+    RawQuery<NT> raw;
+    ask_query(raw, a, x, G);  // before the keys, which they would wait behind
+    auto open_set = [&](const Set& y, int unit) {
         const View& kv = a.rows.kv[y.s];
         f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
         f->table = kv.table;
-        f->last = y.pos0 + (y.nc - 1) / G;
+        f->last = y.pos0 + row_of(a, y.c0 + y.nc - 1);
         f->u = unit;
-        const int page = unit * kElems + half;
-        if (page * kElemKeys <= f->last) ahead = __ldg(kv.table + page);
     };
-    auto open = [&](int elem) {
-        const int page = f->u * kElems + (elem & 1), keys = f->last + 1 - page * kElemKeys;
-        f->elem = elem;
-        f->left = keys <= 0 ? 0 : min(kElemSteps, (keys + kStepKeys - 1) / kStepKeys);
-        f->next = f->heads + (size_t)ahead * n_kv * kTileBytes;
-        if (keys > kElemKeys) ahead = __ldg(f->table + page + 1);
+    auto open = [&](int item) {  // a unit of later rows may lie past the last position of these columns: no steps
+        const int keys = f->last + 1 - f->u * kUnit;
+        f->item = item;
+        f->left = keys <= 0 ? 0 : (min(kUnit, keys) + kStepKeys - 1) / kStepKeys;
+        if (keys > 0) f->next = f->heads + (size_t)__ldg(f->table + f->u * (kUnit / kPage)) * n_kv * kTileBytes;
+        if (keys > kPage) f->page = __ldg(f->table + f->u * (kUnit / kPage) + 1);
     };
-    auto open_next = [&]() {  // the element after f->elem that has keys (a set's last unit may lack a second)
-        while (f->left == 0 && f->elem + 1 < end) {
-            const int elem = f->elem + 1;
-            if ((elem & 1) == 0) {
-                if (f->u * kUnit + kUnit <= f->last) {
-                    ++f->u;
-                } else {
-                    Set y;
-                    const int w = find<1>(a, G, elem >> 1, y);
-                    open_set(y, w, 0);
-                }
-            }
-            open(elem);
+    auto open_next = [&]() {
+        while (f->left == 0 && f->item + 1 < end) {
+            Set y;
+            const int w = find<NT>(a, G, f->item + 1, y);
+            open_set(y, w);
+            open(f->item + 1);
         }
     };
     int fslot = 0;
     auto fetch = [&]() {
         if (lane == 0 && f->left > 0) {
-            ask_step(buf + fslot * kStepBytes, f->next, &f->full[fslot]);
-            f->next += kStepBytes;
+            ask_step(buf + fslot * kStepBytes, f->next, &full[fslot]);
+            const int keys = min(kUnit, f->last + 1 - f->u * kUnit), total = (keys + kStepKeys - 1) / kStepKeys;
             --f->left;
-            open_next();
+            f->next = total - f->left == kPage / kStepKeys ? f->heads + (size_t)f->page * n_kv * kTileBytes : f->next + kStepBytes;
+            if (f->left == 0) open_next();
         }
-        if (++fslot == kDeepStages) fslot = 0;
+        if (++fslot == kStages) fslot = 0;
     };
     if (lane == 0) {
-        for (int k = 0; k < kDeepStages; ++k) mbar_init(&f->full[k], 1);
+        for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
         mbar_init_fence();
-        open_set(x, u, v & 1);
-        open(v);
+        open_set(x, u);
+        open(i);
         open_next();
     }
     __syncwarp();
 #pragma unroll 1
-    for (int k = 0; k < kDeepStages; ++k) fetch();
-    bool fresh = true;  // the set's queries are to be made operands
+    for (int k = 0; k < kStages; ++k) fetch();
+    Query<NT> q;
+    State<NT> e;
     int slot = 0;
     uint32_t phase = 0;
     bool there = true;  // until a wait gives up, which status then says
-    Query<1> q;
-    Elem<1> e;
-    float4 O[8];      // a unit's first element, until its second is there
-    float M[2], L[2];
-    bool held = false;
+    bool fresh = true;  // the set's queries are to be made operands
 #pragma unroll 1
     while (true) {
-        if (fresh) load_query(q, raw, x, G);
-        fresh = false;
-        const int p_first = x.pos0, p_last = x.pos0 + (x.nc - 1) / G;
-        const int k0 = u * kUnit + (v & 1) * kElemKeys, k1 = min(k0 + kElemKeys, p_last + 1);
+        if (fresh) load_query(q, raw, a, x);
+        const int p_first = x.pos0 + row_of(a, x.c0), p_last = x.pos0 + row_of(a, x.c0 + x.nc - 1);
+        const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
         reset(e);
+        auto steps = [&](auto edge) {
 #pragma unroll 1
-        for (int k = k0; k < k1; k += kStepKeys) {
-            there = there && __all_sync(0xffffffffu, mbar_wait(&f->full[slot], phase, a.status));
-            if (!there) continue;  // nothing more is asked for
-            any_step(e, q, buf + slot * kStepBytes, k, p_first, k == k0);
-            __syncwarp();  // the stage has been read
-            fetch();
-            if (++slot == kDeepStages) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
-        finish(e);
-        const bool second = v & 1, ends = v + 1 == end;
-        bool whole = false;  // e.o, e.m, e.l hold a whole unit
-        if (second && !held) {  // for the quarter before
-            float* h = hand + quarter * kHandFloats + lane;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(h - lane)[d * 32 + lane] = f4(e.o[0][d]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                h[1024 + j * 32] = e.m[0][j];
-                h[1024 + (2 + j) * 32] = e.l[0][j];
-            }
-            hand_arrive(quarter);
-        } else if (second || ends) {
-            float w0[2], w1[2];
-            if (second) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) join_weights(M[j], e.m[0][j], L[j], e.l[0][j], w0[j], w1[j]);
-#pragma unroll
-                for (int d = 0; d < 8; ++d) O[d] = join4(O[d], f4(e.o[0][d]), w0, w1);
-            } else {  // a first element at the end: its second is the next quarter's first
-                const float* h = hand + (quarter + 1) * kHandFloats + lane;
-                hand_wait(quarter + 1);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    M[j] = e.m[0][j];
-                    L[j] = e.l[0][j];
-                    join_weights(M[j], h[1024 + j * 32], L[j], h[1024 + (2 + j) * 32], w0[j], w1[j]);
+            for (int k = k0; k < k1; k += kStepKeys) {
+                there = there && __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, a.status));
+                if (!there) continue;  // nothing more is asked for
+                step<NT, decltype(edge)::value>(e, q, buf + slot * kStepBytes, k, k == k0);
+                __syncwarp();  // the stage has been read
+                fetch();
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
                 }
-#pragma unroll
-                for (int d = 0; d < 8; ++d)
-                    O[d] = join4(f4(e.o[0][d]), reinterpret_cast<const float4*>(h - lane)[d * 32 + lane], w0, w1);
             }
-            whole = true;
+        };
+        // one body for all steps of a unit: fetching a second one costs more than it saves
+        if (k0 + kUnit - 1 > p_first)
+            steps(Bool<true>());
+        else
+            steps(Bool<false>());
+        finish(e);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (a.direct) {
+                const OutRows o = out_rows(a, x, G, nt);
+                const float R[2] = {1.f / e.l[nt][0], 1.f / e.l[nt][1]};
+#pragma unroll
+                for (int d = 0; d < 8; ++d) put_out(o, d, f4(e.o[nt][d]), R);
+            } else {
+                const size_t at = partial<NT>(a, x, u) + nt;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = f4(e.o[nt][d]);
+                if (lane < 4) {
+                    *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * lane) = make_float2(e.m[nt][0], e.m[nt][1]);
+                    *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(e.l[nt][0], e.l[nt][1]);
+                }
+            }
+        }
+        if (++i >= end) break;
+        fresh = u + 1 == x.nu;
+        if (fresh) {
+            u = find<NT>(a, G, i, x);
+            ask_query(raw, a, x, G);
         } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                M[j] = e.m[0][j];
-                L[j] = e.l[0][j];
-            }
-#pragma unroll
-            for (int d = 0; d < 8; ++d) O[d] = f4(e.o[0][d]);
-        }
-        held = !second;
-        if (whole) {
-            const size_t at = partial<1>(a, x, u);
-            if (x.nu == 1) {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) put_out(d, O[d], L, [&](int col) { return out_row(a, x, G, col); });
-            } else {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = O[d];
-                put_max_sum(a, at, M, L);
-            }
-        }
-        if (++v >= end) break;
-        if (second) {
-            if (u + 1 < x.nu) {
-                ++u;
-            } else {
-                u = find<1>(a, G, v >> 1, x);
-                ask_query(raw, a, x, G);
-                fresh = true;
-            }
+            ++u;
         }
     }
     if (!there)  // the copies of the other stages end before the CTA does, or these waits run out too
-        for (int k = 1; k < kDeepStages; ++k) {
-            if (++slot == kDeepStages) {
+        for (int k = 1; k < kStages; ++k) {
+            if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1;
             }
-            mbar_wait(&f->full[slot], phase, a.status);
+            mbar_wait(&full[slot], phase, a.status);
         }
 }
 
@@ -900,7 +740,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int nu_s = (a.rows.pos0[s] + R - 1) / kUnit + 1;
     Set x;
     find<NT>(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
-    if (x.nu == 1 || nt * 8 >= x.nc) return;  // written already, or no columns
+    if (nt * 8 >= x.nc) return;  // no columns
     const int groups = (x.nu + kFan - 1) / kFan;
     constexpr int kGroup4 = 36;  // float4 of a group
     pdl_wait();
@@ -946,7 +786,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     } else if (warp) {
         return;
     }
-    put_out(d, O, L, [&](int col) { return out_row(a, x, G, nt * 8 + col); });
+    const float inv[2] = {1.f / L[0], 1.f / L[1]};
+    put_out(out_rows(a, x, G, nt), d, O, inv);
 }
 
 cudaLaunchConfig_t cfg(int grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
@@ -974,9 +815,8 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 int attn_unit() { return kUnit; }
 
 cudaError_t init_attn() {
-    cudaError_t e = allow_smem(wide_kernel<1>, Wide<1>::kBytes);
-    if (e == cudaSuccess) e = allow_smem(wide_kernel<2>, Wide<2>::kBytes);
-    if (e == cudaSuccess) e = allow_smem(deep_kernel, kDeepBytes);
+    cudaError_t e = allow_smem(units_kernel<1>, Cfg<1>::kBytes);
+    if (e == cudaSuccess) e = allow_smem(units_kernel<2>, Cfg<2>::kBytes);
     if (e == cudaSuccess) e = allow_smem(join_kernel<1>, kMaxJoinBytes);
     if (e == cudaSuccess) e = allow_smem(join_kernel<2>, kMaxJoinBytes);
     return e;
@@ -986,6 +826,7 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
     const Rows& m = a.rows;
     const int G = a.group = a.n_q / m.n_kv;
+    a.group_inv = (65536 + G - 1) / G;
     // one tile of eight columns where every stream's rows fit it, else two: codes are then unpacked once for 16 columns
     int nt = 1, most = 1;
     for (int s = 0; s < m.n_streams; ++s)
@@ -1004,14 +845,14 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
         }
     }
     a.item_start[m.n_streams] = items;
-    const bool deep = nt == 1 && items >= kDeepUnits * kDeepCtas * sms;
+    // a full grid, or as many warps as there are units
+    const int ctas = nt == 1 ? Cfg<1>::kCtas : Cfg<2>::kCtas, full = sms * ctas, need = (items + kWarps - 1) / kWarps;
+    a.per_sm = need < full ? 1 : ctas;
+    a.direct = most == 1;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = deep ? cfg(sms * kDeepCtas, kDeepWarps * 32, kDeepBytes, st, attr, pdl)
-                                : cfg(items, kWideWarps * 32, nt == 1 ? Wide<1>::kBytes : Wide<2>::kBytes, st, attr, pdl);
-    cudaError_t e = deep      ? cudaLaunchKernelEx(&c, deep_kernel, a)
-                    : nt == 1 ? cudaLaunchKernelEx(&c, wide_kernel<1>, a)
-                              : cudaLaunchKernelEx(&c, wide_kernel<2>, a);
-    if (e != cudaSuccess || most == 1) return e;
+    cudaLaunchConfig_t c = cfg(need < full ? need : full, kWarps * 32, nt == 1 ? Cfg<1>::kBytes : Cfg<2>::kBytes, st, attr, pdl);
+    const cudaError_t e = nt == 1 ? cudaLaunchKernelEx(&c, units_kernel<1>, a) : cudaLaunchKernelEx(&c, units_kernel<2>, a);
+    if (e != cudaSuccess || a.direct) return e;
     const int groups = (most + kFan - 1) / kFan;
     c = cfg(sets * m.n_kv * nt * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
             st, attr, true);
