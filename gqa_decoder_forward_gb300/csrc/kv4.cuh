@@ -48,15 +48,17 @@ struct View {
 };
 
 // Rows of one call, grouped by stream: rows [row_start[s], row_start[s+1])
-// belong to stream s and sit at positions pos0[s], pos0[s]+1, ...
+// belong to stream s and sit at positions pos0[s], pos0[s]+1, ...  (Attention may cut
+// a call's streams in two: room for twice as many.)
+constexpr int kMaxParts = 2 * kMaxStreams;
 struct Rows {
     int n_streams;
     int n_rows;
     int n_kv;
     int layer;
-    int row_start[kMaxStreams + 1];
-    int pos0[kMaxStreams];
-    View kv[kMaxStreams];
+    int row_start[kMaxParts + 1];
+    int pos0[kMaxParts];
+    View kv[kMaxParts];
 };
 
 __device__ __forceinline__ int stream_of(const Rows& m, int r) {
@@ -112,10 +114,10 @@ struct AttnArgs {
     int group;           // set by launch_attn: query heads per KV head,
     int group_inv;       // 65536 / group, rounded up,
     int per_sm, direct;  // CTAs of an SM; every stream has one unit, whose warp writes the output,
-    int item_start[kMaxStreams + 1]; // first unit (over its sets) of a stream,
-    int set_start[kMaxStreams];       // and its first set of columns
+    int item_start[kMaxParts + 1]; // first unit (over its sets) of a stream,
+    int set_start[kMaxParts + 1];       // and its first set of columns
 };
-int attn_unit();         // keys of one partial
+int attn_max_units(int positions);  // partials of a row's head over caches of up to so many positions
 cudaError_t init_attn();
 cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl);
 

@@ -30,6 +30,7 @@
 // call's units one after the other, and meets no other warp.  A warp's keys come by
 // bulk copies that one of its lanes asks for, into shared memory that no other warp
 // reads, always kStages - 1 steps ahead.
+#include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
 
@@ -43,17 +44,21 @@ namespace {
 
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
-constexpr int kUnit = 256;                         // keys of a unit
+// Keys of a unit, by the position of the row that attends: more keys mean fewer starts
+// and partials, fewer mean more warps for one short cache.  Measured for one 33B-shaped row
+// and layer: UNITTEXT
+constexpr int kShortUnit = 128, kLongUnit = 256, kLongFrom = 8192;
+__host__ __device__ constexpr int unit_of(int pos) { return pos < kLongFrom ? kShortUnit : kLongUnit; }
 constexpr int kWarps = 4;                          // of a CTA
 #ifndef DC
-#define DC 4
+#define DC 3
 #define DS 3
 #endif
 constexpr int kCtas1 = DC, kStages1 = DS;          // CTAs of an SM and steps of a warp's ring, one tile of columns
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
-constexpr int kMaxJoinBytes = ((1 << 20) / kUnit + kFan - 1) / kFan * kGroupBytes;
+constexpr int kMaxJoinBytes = ((1 << 20) / kLongUnit + kFan - 1) / kFan * kGroupBytes;
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
@@ -406,6 +411,7 @@ __device__ __forceinline__ int row_of(const AttnArgs& a, int c) { return (c * a.
 struct Set {
     int s, h, c0, nc;      // columns c0 .. c0 + nc - 1 of stream s
     int r0, pos0, nu, id;  // the stream's first row and position, its units; the set's partials
+    int unit;              // keys of a unit
 };
 
 // Item `i` of the call's units in order of stream, columns, KV head, unit; returns the unit.
@@ -419,7 +425,8 @@ __device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
     x.s = s;
     x.r0 = rm.row_start[s];
     x.pos0 = rm.pos0[s];
-    x.nu = (int)((unsigned)(x.pos0 + R - 1) / kUnit) + 1;
+    x.unit = unit_of(x.pos0);
+    x.nu = (x.pos0 + R - 1) / x.unit + 1;
     const unsigned sh = (unsigned)i / (unsigned)x.nu, chunk = sh / (unsigned)rm.n_kv;
     const int u = i - (int)sh * x.nu;
     x.h = sh - chunk * rm.n_kv;
@@ -529,9 +536,8 @@ __device__ __forceinline__ void put_out(const OutRows& o, int d, float4 O, const
 // The fetching side of a warp: lane 0, its state in shared memory.
 struct Fetch {
     const char *next, *heads;  // the step to fetch; tile 0 of the layer and head
-    const int* table;
     int item, left;            // the unit, its steps not yet fetched
-    int u, last;               // its number in the set, the set's last position
+    int last, k;               // the set's last position, the position of the step to fetch
     int page;                  // the unit's second page
 };
 
@@ -569,35 +575,32 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
     int u = find<NT>(a, G, i, x);
     RawQuery<NT> raw;
     ask_query(raw, a, x, G);  // before the keys, which they would wait behind
-    auto open_set = [&](const Set& y, int unit) {
+    auto open = [&](int item, const Set& y, int v) {
         const View& kv = a.rows.kv[y.s];
         f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
-        f->table = kv.table;
-        f->last = y.pos0 + row_of(a, y.c0 + y.nc - 1);
-        f->u = unit;
-    };
-    auto open = [&](int item) {  // a unit of later rows may lie past the last position of these columns: no steps
-        const int keys = f->last + 1 - f->u * kUnit;
+        const int last = y.pos0 + row_of(a, y.c0 + y.nc - 1), k = v * y.unit, keys = last + 1 - k;
         f->item = item;
-        f->left = keys <= 0 ? 0 : (min(kUnit, keys) + kStepKeys - 1) / kStepKeys;
-        if (keys > 0) f->next = f->heads + (size_t)__ldg(f->table + f->u * (kUnit / kPage)) * n_kv * kTileBytes;
-        if (keys > kPage) f->page = __ldg(f->table + f->u * (kUnit / kPage) + 1);
+        f->k = k;
+        // a unit of later rows may lie past the last position of these columns: no steps
+        f->left = keys <= 0 ? 0 : (min(y.unit, keys) + kStepKeys - 1) / kStepKeys;
+        const int* table = kv.table + k / kPage;
+        if (keys > 0) f->next = f->heads + (size_t)__ldg(table) * n_kv * kTileBytes + k % kPage / kBlockPos * kBlockBytes;
+        if (min(y.unit, keys) > kPage) f->page = __ldg(table + 1);  // units of more than a page begin with one
     };
     auto open_next = [&]() {
         while (f->left == 0 && f->item + 1 < end) {
             Set y;
             const int w = find<NT>(a, G, f->item + 1, y);
-            open_set(y, w);
-            open(f->item + 1);
+            open(f->item + 1, y, w);
         }
     };
     int fslot = 0;
     auto fetch = [&]() {
         if (lane == 0 && f->left > 0) {
             ask_step(buf + fslot * kStepBytes, f->next, &full[fslot]);
-            const int keys = min(kUnit, f->last + 1 - f->u * kUnit), total = (keys + kStepKeys - 1) / kStepKeys;
+            f->k += kStepKeys;
+            f->next = f->k % kPage == 0 ? f->heads + (size_t)f->page * n_kv * kTileBytes : f->next + kStepBytes;
             --f->left;
-            f->next = total - f->left == kPage / kStepKeys ? f->heads + (size_t)f->page * n_kv * kTileBytes : f->next + kStepBytes;
             if (f->left == 0) open_next();
         }
         if (++fslot == kStages) fslot = 0;
@@ -605,8 +608,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
     if (lane == 0) {
         for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
         mbar_init_fence();
-        open_set(x, u);
-        open(i);
+        open(i, x, u);
         open_next();
     }
     __syncwarp();
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
     while (true) {
         if (fresh) load_query(q, raw, a, x);
         const int p_first = x.pos0 + row_of(a, x.c0), p_last = x.pos0 + row_of(a, x.c0 + x.nc - 1);
-        const int k0 = u * kUnit, k1 = min(k0 + kUnit, p_last + 1);
+        const int k0 = u * x.unit, k1 = min(k0 + x.unit, p_last + 1);
         reset(e);
         auto steps = [&](auto edge) {
 #pragma unroll 1
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
             }
         };
         // one body for all steps of a unit: fetching a second one costs more than it saves
-        if (k0 + kUnit - 1 > p_first)
+        if (k0 + x.unit - 1 > p_first)
             steps(Bool<true>());
         else
             steps(Bool<false>());
@@ -696,29 +698,27 @@ __device__ __forceinline__ void join(const float* pm, const float* pl, const flo
         l[r] = in ? __ldcg(pl + (size_t)(4 * r + a) * stride * 8 + c) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < kFan; ++i)
-        if (i < n) v[i] = __ldcg(po + (size_t)i * stride * 256);
+    for (int i = 0; i < kFan; ++i) v[i] = __ldcg(po + (size_t)min(i, n - 1) * stride * 256);  // past n: weight 0 below
     float top = m[0];
 #pragma unroll
     for (int r = 1; r < kR; ++r) top = fmaxf(top, m[r]);
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
 #pragma unroll
-    for (int r = 0; r < kR; ++r) m[r] = ex2(m[r] - top);  // the partial's weight
+    for (int r = 0; r < kR; ++r) m[r] = 4 * r + a < n ? ex2(m[r] - top) : 0.f;  // the partial's weight
     L[0] = L[1] = 0.f;
     O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kFan; ++i)
-        if (i < n) {
-            const int from = (i & 3) * 8 + 2 * t;
-            const float w0 = __shfl_sync(0xffffffffu, m[i >> 2], from), w1 = __shfl_sync(0xffffffffu, m[i >> 2], from + 1);
-            L[0] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from), w0, L[0]);
-            L[1] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from + 1), w1, L[1]);
-            O.x = fmaf(v[i].x, w0, O.x);
-            O.y = fmaf(v[i].y, w1, O.y);
-            O.z = fmaf(v[i].z, w0, O.z);
-            O.w = fmaf(v[i].w, w1, O.w);
-        }
+    for (int i = 0; i < kFan; ++i) {
+        const int from = (i & 3) * 8 + 2 * t;
+        const float w0 = __shfl_sync(0xffffffffu, m[i >> 2], from), w1 = __shfl_sync(0xffffffffu, m[i >> 2], from + 1);
+        L[0] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from), w0, L[0]);
+        L[1] = fmaf(__shfl_sync(0xffffffffu, l[i >> 2], from + 1), w1, L[1]);
+        O.x = fmaf(v[i].x, w0, O.x);
+        O.y = fmaf(v[i].y, w1, O.y);
+        O.z = fmaf(v[i].z, w0, O.z);
+        O.w = fmaf(v[i].w, w1, O.w);
+    }
     M[0] = __shfl_sync(0xffffffffu, top, 2 * t);
     M[1] = __shfl_sync(0xffffffffu, top, 2 * t + 1);
 }
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     int s = 0;
     while (s + 1 < a.rows.n_streams && set >= a.set_start[s + 1] * a.rows.n_kv) ++s;
     const int R = a.rows.row_start[s + 1] - a.rows.row_start[s];
-    const int nu_s = (a.rows.pos0[s] + R - 1) / kUnit + 1;
+    const int nu_s = (a.rows.pos0[s] + R - 1) / unit_of(a.rows.pos0[s]) + 1;
     Set x;
     find<NT>(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
     if (nt * 8 >= x.nc) return;  // no columns
@@ -747,6 +747,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     pdl_trigger();
     float M[2], L[2];
     float4 O;
+#pragma unroll 1
     for (int gi = warp; gi < groups; gi += blockDim.x / 32) {
         const size_t at = partial<NT>(a, x, gi * kFan) + nt;
         join(a.pm + at * 8, a.pl + at * 8, reinterpret_cast<const float4*>(a.po) + at * 256 + d * 32 + lane,
@@ -764,6 +765,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         __syncthreads();
         if (warp) return;
         M[0] = M[1] = kUnset;
+#pragma unroll 4
         for (int gi = 0; gi < groups; ++gi) {
             const float2 m = reinterpret_cast<const float2*>(js + gi * kGroup4 + 32)[t];
             M[0] = fmaxf(M[0], m.x);
@@ -771,6 +773,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         }
         L[0] = L[1] = 0.f;
         O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int gi = 0; gi < groups; ++gi) {
             const float2* ml = reinterpret_cast<const float2*>(js + gi * kGroup4 + 32);
             const float2 m = ml[t], l = ml[4 + t];
@@ -812,7 +815,10 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 
 }  // namespace
 
-int attn_unit() { return kUnit; }
+int attn_max_units(int positions) {
+    const int short_ = (std::min(positions, kLongFrom) + kShortUnit - 1) / kShortUnit;
+    return std::max(short_, (positions + kLongUnit - 1) / kLongUnit);
+}
 
 cudaError_t init_attn() {
     cudaError_t e = allow_smem(units_kernel<1>, Cfg<1>::kBytes);
@@ -824,7 +830,20 @@ cudaError_t init_attn() {
 
 cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
-    const Rows& m = a.rows;
+    // a stream whose rows lie on both sides of a change of the unit's size becomes two
+    Rows& m = a.rows;
+    for (int s = 0; s < m.n_streams; ++s) {
+        const int R = m.row_start[s + 1] - m.row_start[s], before = kLongFrom - m.pos0[s];
+        if (R < 2 || before <= 0 || before >= R) continue;
+        for (int t = m.n_streams; t > s; --t) {
+            m.row_start[t + 1] = m.row_start[t];
+            m.pos0[t] = m.pos0[t - 1];
+            m.kv[t] = m.kv[t - 1];
+        }
+        m.row_start[s + 1] = m.row_start[s] + before;
+        m.pos0[s + 1] = kLongFrom;
+        ++m.n_streams;
+    }
     const int G = a.group = a.n_q / m.n_kv;
     a.group_inv = (65536 + G - 1) / G;
     // one tile of eight columns where every stream's rows fit it, else two: codes are then unpacked once for 16 columns
@@ -839,7 +858,7 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
         a.set_start[s] = sets;
         sets += chunks;
         if (R > 0) {
-            const int nu = (m.pos0[s] + R - 1) / kUnit + 1;
+            const int nu = (m.pos0[s] + R - 1) / unit_of(m.pos0[s]) + 1;
             items += chunks * m.n_kv * nu;
             if (nu > most) most = nu;
         }
