@@ -71,9 +71,9 @@ AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
     AttnLayout L;
     L.units = kv4::attn_max_units(max_positions);
     // Tiles of eight columns over all sets.  A call has at most 16 streams, cut into 32 parts; a part
-    // of R rows has one tile per KV head if every part's R G columns fit one, else 2 ceil(R G / 16).
+    // of R rows has ceil(R G / 8) tiles per KV head.
     const int G = n_q / n_kv;
-    const size_t tiles = (size_t)n_kv * 2 * (std::min(max_rows, kv4::kMaxParts) + (max_rows * G + 15) / 16);
+    const size_t tiles = (size_t)n_kv * (std::min(max_rows, kv4::kMaxParts) + max_rows * G / 8);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t o = off;

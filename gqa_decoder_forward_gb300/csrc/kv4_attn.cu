@@ -23,7 +23,7 @@
 // of the largest.  Likewise m moves only when an x_t passes it by 8.  Both decisions
 // are a column's own, so a column's bits do not depend on its neighbours.
 //
-// Split.  A unit is 256 keys of a KV head at absolute positions, taken by one warp in
+// Split.  A unit is 128 or 256 keys of a KV head and up to eight columns at absolute positions, taken by one warp in
 // steps of 32 with a fresh (m, l, c, output).  A second kernel joins the units: groups
 // of 16, then the groups, in order.  So the bits depend on the position alone, however
 // the units are spread: the grid is persistent, each warp takes an equal share of the
@@ -45,16 +45,14 @@ namespace {
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
 // Keys of a unit, by the position of the row that attends: more keys mean fewer starts
-// and partials, fewer mean more warps for one short cache.  Measured for one 33B-shaped row
-// and layer: UNITTEXT
+// and partials, fewer mean more warps for one short cache.  One layer of 8 KV heads, seven
+// query heads each, with 256 | 128 | 64 keys before position 8,192: one row over 4,096 keys
+// 12.4 | 8.9 | 7.7 us, 16 rows over 8,192 each 34.1 | 34.3 | 45.6 us.  With 256 | 128 from
+// there on: one row over 131,072 keys 43.2 | 47.9 us.
 constexpr int kShortUnit = 128, kLongUnit = 256, kLongFrom = 8192;
 __host__ __device__ constexpr int unit_of(int pos) { return pos < kLongFrom ? kShortUnit : kLongUnit; }
 constexpr int kWarps = 4;                          // of a CTA
-#ifndef DC
-#define DC 3
-#define DS 3
-#endif
-constexpr int kCtas1 = DC, kStages1 = DS;          // CTAs of an SM and steps of a warp's ring, one tile of columns
+constexpr int kCtas = 3, kStages = 3;              // CTAs of an SM, steps of a warp's ring
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
@@ -139,52 +137,44 @@ __device__ __forceinline__ float col_sum(float x) {
 // the layout of every partial output, in registers, shared and global memory
 // ([tile][8][lane] of float4), until the last join writes rows of dims.
 
-template <int NT>
 struct Query {
-    uint32_t b[NT][8][2];  // q' as operands: [word of a key's row x weight of its codes]
-    float Q0[NT][2], Q1[NT][2], F[NT][2];
-    int pos[NT][2];        // position of the column's row, -1 for a column past the last
+    uint32_t b[8][2];  // q' as operands: [word of a key's row x weight of its codes]
+    float Q0[2], Q1[2], F[2];
+    int pos[2];        // position of the column's row, -1 for a column past the last
 };
 
-template <int NT>
 struct State {
-    float m[NT][2], l[NT][2], c[NT][2], za[NT][2][2];  // l and za: this lane's keys only
-    float o[NT][8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
+    float m[2], l[2], c[2], za[2][2];  // l and za: this lane's keys only
+    float o[8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
 };
 
-template <int NT>
-__device__ __forceinline__ void reset(State<NT>& e) {
+__device__ __forceinline__ void reset(State& e) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            e.m[nt][j] = kUnset;
-            e.l[nt][j] = 0.f;
-            e.c[nt][j] = pow2(100);
-            e.za[nt][j][0] = e.za[nt][j][1] = 0.f;
-        }
-#pragma unroll
-        for (int d = 0; d < 8; ++d) e.o[nt][d][0] = e.o[nt][d][1] = e.o[nt][d][2] = e.o[nt][d][3] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+        e.m[j] = kUnset;
+        e.l[j] = 0.f;
+        e.c[j] = pow2(100);
+        e.za[j][0] = e.za[j][1] = 0.f;
     }
+#pragma unroll
+    for (int d = 0; d < 8; ++d) e.o[d][0] = e.o[d][1] = e.o[d][2] = e.o[d][3] = 0.f;
 }
 
 // The 32 keys from position k0, whose two blocks are at buf.  EDGE: some column does
 // not see all of them; what it does not see takes no part, whatever its bytes.
 // first: the unit's first step.  (A body of its own for that costs more in
 // instruction cache misses than its tests.)
-template <int NT, bool EDGE>
-__device__ __forceinline__ void step(State<NT>& e, const Query<NT>& q, const char* buf, int k0, bool first) {
+template <bool EDGE>
+__device__ __forceinline__ void step(State& e, const Query& q, const char* buf, int k0, bool first) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int krow = key_of_row(g);  // rows g and g + 8 of the tiles: keys krow, krow + 8
     const int k_at = krow * kRowBytes + ((t ^ (krow & 2)) << 4);
     // ---- code sums of the scores, a group of dims apart ----
-    float acc[2][NT][2][4];
+    float acc[2][2][4];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[b][nt][0][i] = acc[b][nt][1][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[b][0][i] = acc[b][1][i] = 0.f;
         const uint4 ka = *reinterpret_cast<const uint4*>(buf + b * kBlockBytes + k_at);
         const uint4 kc = *reinterpret_cast<const uint4*>(buf + b * kBlockBytes + k_at + 8 * kRowBytes);
         const uint32_t x[4] = {ka.x, ka.y, ka.z, ka.w}, y[4] = {kc.x, kc.y, kc.z, kc.w};
@@ -193,11 +183,8 @@ __device__ __forceinline__ void step(State<NT>& e, const Query<NT>& q, const cha
             const Codes cx = codes(x[w]), cy = codes(y[w]);
             const uint32_t hx0 = hi_codes(cx.both[0], cx.lo[0]), hx1 = hi_codes(cx.both[1], cx.lo[1]);
             const uint32_t hy0 = hi_codes(cy.both[0], cy.lo[0]), hy1 = hi_codes(cy.both[1], cy.lo[1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(acc[b][nt][w & 1], cx.lo[0], cy.lo[0], cx.lo[1], cy.lo[1], q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
-                mma_f16(acc[b][nt][w & 1], hx0, hy0, hx1, hy1, q.b[nt][2 * w + 1][0], q.b[nt][2 * w + 1][1]);
-            }
+            mma_f16(acc[b][w & 1], cx.lo[0], cy.lo[0], cx.lo[1], cy.lo[1], q.b[2 * w][0], q.b[2 * w][1]);
+            mma_f16(acc[b][w & 1], hx0, hy0, hx1, hy1, q.b[2 * w + 1][0], q.b[2 * w + 1][1]);
         }
     }
     // ---- scores and weights: [block][key half][column] ----
@@ -208,137 +195,134 @@ __device__ __forceinline__ void step(State<NT>& e, const Query<NT>& q, const cha
     auto v_meta = [&](int b, int hk) {
         return *reinterpret_cast<const uint2*>(meta + kHalfBlock + b * kBlockBytes + hk * 8 * kMetaBytes);
     };
-    uint32_t wb[NT][2][2][2];  // weights' operands [block][group][key half]
+    uint32_t wb[2][2][2];  // weights' operands [block][group][key half]
+    // rows of this lane a column does not see
+    auto hidden = [&](int j, int b, int hk) { return k0 + 16 * b + 8 * hk + krow > q.pos[j]; };
+    float p[2][2][2], raw[2][2][2], top[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        // rows of this lane a column does not see
-        auto hidden = [&](int j, int b, int hk) { return k0 + 16 * b + 8 * hk + krow > q.pos[nt][j]; };
-        float p[2][2][2], raw[2][2][2], top[2];
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk) {
+            const uint2 km = k_meta(b, hk);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float ts = fmaf(lo_f(km.y), acc[b][1][2 * hk + j], lo_f(km.x) * acc[b][0][2 * hk + j]);
+                const float z = fmaf(hi_f(km.y), q.Q1[j], hi_f(km.x) * q.Q0[j]);
+                raw[b][hk][j] = fmaf(q.F[j], ts, z);
+            }
+        }
+    if (EDGE) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int hk = 0; hk < 2; ++hk)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (hidden(j, b, hk)) raw[b][hk][j] = -INFINITY;
+    }
+    auto weights = [&](int b, int hk) {  // w = P c s
+        const uint2 vm = v_meta(b, hk);
+        float w[2][2];  // [group][column]
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float pc = p[b][hk][j] * e.c[j];
+            w[0][j] = pc * lo_f(vm.x);
+            w[1][j] = pc * lo_f(vm.y);
+        }
+        if (EDGE) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (hidden(j, b, hk)) w[0][j] = w[1][j] = 0.f;
+        }
+        wb[b][0][hk] = pack_half(w[0][0], w[0][1]);
+        wb[b][1][hk] = pack_half(w[1][0], w[1][1]);
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        top[j] = fmaxf(fmaxf(raw[0][0][j], raw[0][1][j]), fmaxf(raw[1][0][j], raw[1][1][j]));
+    bool move = first;
+    if (!first) {
+        uint32_t top2 = 0;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int hk = 0; hk < 2; ++hk) {
-                const uint2 km = k_meta(b, hk);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float ts = fmaf(lo_f(km.y), acc[b][nt][1][2 * hk + j], lo_f(km.x) * acc[b][nt][0][2 * hk + j]);
-                    const float z = fmaf(hi_f(km.y), q.Q1[nt][j], hi_f(km.x) * q.Q0[nt][j]);
-                    raw[b][hk][j] = fmaf(q.F[nt][j], ts, z);
-                }
+                for (int j = 0; j < 2; ++j) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[j]);
+                weights(b, hk);
+                // w >= 0: fp16 order is the order of the bits
+                top2 = __vimax3_u16x2(top2, wb[b][0][hk], wb[b][1][hk]);
             }
-        if (EDGE) {
+        // 2^15 is 0x7800 (a NaN, above it, counts too and stays one)
+        move = __any_sync(0xffffffffu, top[0] > e.m[0] + kLazy || top[1] > e.m[1] + kLazy ||
+                                           (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
+    }
+    // A score passes m by more than 8, or a w passes 2^15: m, c and the running sums move in the
+    // columns where it does.  A unit's first step sets them.
+    if (move) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float high = col_max(top[j]);
+            float al = 1.f;
+            if (high > e.m[j] + kLazy) {
+                al = ex2(e.m[j] - high);
+                e.m[j] = high;
+                e.l[j] *= al;
+                e.za[j][0] *= al;
+                e.za[j][1] *= al;
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int hk = 0; hk < 2; ++hk)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (hidden(j, b, hk)) raw[b][hk][j] = -INFINITY;
-        }
-        auto weights = [&](int b, int hk) {  // w = P c s
-            const uint2 vm = v_meta(b, hk);
-            float w[2][2];  // [group][column]
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float pc = p[b][hk][j] * e.c[nt][j];
-                w[0][j] = pc * lo_f(vm.x);
-                w[1][j] = pc * lo_f(vm.y);
-            }
-            if (EDGE) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (hidden(j, b, hk)) w[0][j] = w[1][j] = 0.f;
-            }
-            wb[nt][b][0][hk] = pack_half(w[0][0], w[0][1]);
-            wb[nt][b][1][hk] = pack_half(w[1][0], w[1][1]);
-        };
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            top[j] = fmaxf(fmaxf(raw[0][0][j], raw[0][1][j]), fmaxf(raw[1][0][j], raw[1][1][j]));
-        bool move = first;
-        if (!first) {
-            uint32_t top2 = 0;
+                for (int hk = 0; hk < 2; ++hk) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[j]);
+            float ps = 0.f;  // largest P s 2^-20 (which cannot overflow)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[nt][j]);
-                    weights(b, hk);
-                    // w >= 0: fp16 order is the order of the bits
-                    top2 = __vimax3_u16x2(top2, wb[nt][b][0][hk], wb[nt][b][1][hk]);
+                    const uint2 vm = v_meta(b, hk);
+                    const float x = p[b][hk][j] * (fmaxf(lo_f(vm.x), lo_f(vm.y)) * pow2(-20));
+                    if (!EDGE || !hidden(j, b, hk)) ps = fmaxf(ps, x);
                 }
-            // 2^15 is 0x7800 (a NaN, above it, counts too and stays one)
-            move = __any_sync(0xffffffffu, top[0] > e.m[nt][0] + kLazy || top[1] > e.m[nt][1] + kLazy ||
-                                               (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
-        }
-        // A score passes m by more than 8, or a w passes 2^15: m, c and the running sums move in the
-        // columns where it does.  A unit's first step sets them.
-        if (move) {
+            ps = col_max(ps);
+            if (ps * e.c[j] > kTopW * pow2(-20) && ps < INFINITY) {
+                const float c = pow2(max(-100, min(100, 6 - 20 - exponent(ps))));
+                al *= c * inv_pow2(e.c[j]);  // powers of two: exact, or 0
+                e.c[j] = c;
+            }
+            if (!first) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float high = col_max(top[j]);
-                float al = 1.f;
-                if (high > e.m[nt][j] + kLazy) {
-                    al = ex2(e.m[nt][j] - high);
-                    e.m[nt][j] = high;
-                    e.l[nt][j] *= al;
-                    e.za[nt][j][0] *= al;
-                    e.za[nt][j][1] *= al;
-                }
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[nt][j]);
-                float ps = 0.f;  // largest P s 2^-20 (which cannot overflow)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
-                        const uint2 vm = v_meta(b, hk);
-                        const float x = p[b][hk][j] * (fmaxf(lo_f(vm.x), lo_f(vm.y)) * pow2(-20));
-                        if (!EDGE || !hidden(j, b, hk)) ps = fmaxf(ps, x);
-                    }
-                ps = col_max(ps);
-                if (ps * e.c[nt][j] > kTopW * pow2(-20) && ps < INFINITY) {
-                    const float c = pow2(max(-100, min(100, 6 - 20 - exponent(ps))));
-                    al *= c * inv_pow2(e.c[nt][j]);  // powers of two: exact, or 0
-                    e.c[nt][j] = c;
-                }
-                if (!first) {
-#pragma unroll
-                    for (int d = 0; d < 8; ++d) {
-                        e.o[nt][d][j] *= al;
-                        e.o[nt][d][2 + j] *= al;
-                    }
+                for (int d = 0; d < 8; ++d) {
+                    e.o[d][j] *= al;
+                    e.o[d][2 + j] *= al;
                 }
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int hk = 0; hk < 2; ++hk) weights(b, hk);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int hk = 0; hk < 2; ++hk) {
-                const uint2 vm = v_meta(b, hk);
-                float z[2][2] = {{hi_f(vm.x), hi_f(vm.y)}, {hi_f(vm.x), hi_f(vm.y)}};  // [column][group]
-                if (EDGE) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (hidden(j, b, hk)) z[j][0] = z[j][1] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    e.l[nt][j] += p[b][hk][j];
-                    e.za[nt][j][0] = fmaf(p[b][hk][j], z[j][0], e.za[nt][j][0]);
-                    e.za[nt][j][1] = fmaf(p[b][hk][j], z[j][1], e.za[nt][j][1]);
-                }
-#pragma unroll
-                for (int gr = 0; gr < 2; ++gr) wb[nt][b][gr][hk] = wm::movmatrix_t(wb[nt][b][gr][hk]);
-            }
+            for (int hk = 0; hk < 2; ++hk) weights(b, hk);
     }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk) {
+            const uint2 vm = v_meta(b, hk);
+            float z[2][2] = {{hi_f(vm.x), hi_f(vm.y)}, {hi_f(vm.x), hi_f(vm.y)}};  // [column][group]
+            if (EDGE) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (hidden(j, b, hk)) z[j][0] = z[j][1] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                e.l[j] += p[b][hk][j];
+                e.za[j][0] = fmaf(p[b][hk][j], z[j][0], e.za[j][0]);
+                e.za[j][1] = fmaf(p[b][hk][j], z[j][1], e.za[j][1]);
+            }
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) wb[b][gr][hk] = wm::movmatrix_t(wb[b][gr][hk]);
+        }
     // ---- code sums of the output ----
     const char* vb = buf + kHalfBlock + ((g ^ ((t & 2) << 1)) << 3);
 #pragma unroll
@@ -354,14 +338,11 @@ __device__ __forceinline__ void step(State<NT>& e, const Query<NT>& q, const cha
             const uint32_t x2 = __byte_perm(e2, e3, 0x5410), x3 = __byte_perm(e2, e3, 0x7632);
             const Codes y0 = codes(x0), y1 = codes(x1), y2 = codes(x2), y3 = codes(x3);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(e.o[nt][gr * 4 + 2 * i], y0.lo[i], y1.lo[i], y2.lo[i], y3.lo[i], wb[nt][b][gr][0],
-                            wb[nt][b][gr][1]);
-                    mma_f16(e.o[nt][gr * 4 + 2 * i + 1], y0.both[i], y1.both[i], y2.both[i], y3.both[i],
-                            wb[nt][b][gr][0], wb[nt][b][gr][1]);
-                }
+            for (int i = 0; i < 2; ++i) {
+                mma_f16(e.o[gr * 4 + 2 * i], y0.lo[i], y1.lo[i], y2.lo[i], y3.lo[i], wb[b][gr][0], wb[b][gr][1]);
+                mma_f16(e.o[gr * 4 + 2 * i + 1], y0.both[i], y1.both[i], y2.both[i], y3.both[i], wb[b][gr][0],
+                        wb[b][gr][1]);
+            }
         }
     }
 }
@@ -378,23 +359,20 @@ __device__ __forceinline__ void ask_step(char* dst, const char* src, uint64_t* f
 // A unit's end, in place: l over the column's lanes, o from code units and c to the
 // output's own scale, the zeros' sums added.  Of the pairs of tiles, the whole bytes
 // less the low codes leave the high ones.
-template <int NT>
-__device__ __forceinline__ void finish(State<NT>& e) {
+__device__ __forceinline__ void finish(State& e) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int j = 0; j < 2; ++j) {
+        e.l[j] = col_sum(e.l[j]);
+        const float z[2] = {col_sum(e.za[j][0]), col_sum(e.za[j][1])};
+        const float inv = inv_pow2(e.c[j]), lo = inv * kLoCode, hi = inv * kHiCode;  // c >= 2^-100
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            e.l[nt][j] = col_sum(e.l[nt][j]);
-            const float z[2] = {col_sum(e.za[nt][j][0]), col_sum(e.za[nt][j][1])};
-            const float inv = inv_pow2(e.c[nt][j]), lo = inv * kLoCode, hi = inv * kHiCode;  // c >= 2^-100
+        for (int d = 0; d < 8; d += 2)
 #pragma unroll
-            for (int d = 0; d < 8; d += 2)
-#pragma unroll
-                for (int k = j; k < 4; k += 2) {
-                    e.o[nt][d + 1][k] = fmaf(e.o[nt][d + 1][k] - e.o[nt][d][k], hi, z[d >> 2]);
-                    e.o[nt][d][k] = fmaf(e.o[nt][d][k], lo, z[d >> 2]);
-                }
-        }
+            for (int k = j; k < 4; k += 2) {
+                e.o[d + 1][k] = fmaf(e.o[d + 1][k] - e.o[d][k], hi, z[d >> 2]);
+                e.o[d][k] = fmaf(e.o[d][k], lo, z[d >> 2]);
+            }
+    }
 }
 
 template <bool B>
@@ -415,7 +393,6 @@ struct Set {
 };
 
 // Item `i` of the call's units in order of stream, columns, KV head, unit; returns the unit.
-template <int NT>
 __device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
     const Rows& rm = a.rows;
     int s = 0;
@@ -430,80 +407,70 @@ __device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
     const unsigned sh = (unsigned)i / (unsigned)x.nu, chunk = sh / (unsigned)rm.n_kv;
     const int u = i - (int)sh * x.nu;
     x.h = sh - chunk * rm.n_kv;
-    x.c0 = chunk * NT * 8;
-    x.nc = min(NT * 8, R * G - x.c0);
+    x.c0 = chunk * 8;
+    x.nc = min(8, R * G - x.c0);
     x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
     return u;
 }
 
-template <int NT>
 __device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u) {
-    return ((size_t)x.id * a.max_units + u) * NT;
+    return (size_t)x.id * a.max_units + u;
 }
 
 // The queries of a set: asked for (ask_query) before the keys, which they would
 // otherwise wait behind, and made operands (load_query) when they are there.  Lane
 // (g, t) holds column g's dims of its words of a key's row: 16t..16t+15 and 64+16t..64+16t+15.
-template <int NT>
 struct RawQuery {
-    uint4 w[NT][4];
+    uint4 w[4];
 };
-template <int NT>
-__device__ __forceinline__ void ask_query(RawQuery<NT>& r, const AttnArgs& a, const Set& x, int G) {
+__device__ __forceinline__ void ask_query(RawQuery& r, const AttnArgs& a, const Set& x, int G) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int c = x.c0 + g;
+    const bool in = g < x.nc;
+    const bf16* q = a.q + (in ? (long)(x.r0 + row_of(a, c)) * a.ldq + (x.h * G + c - row_of(a, c) * G) * kHeadDim : 0) + 16 * t;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int c = x.c0 + nt * 8 + g;
-        const bool in = nt * 8 + g < x.nc;
-        const bf16* q = a.q + (in ? (long)(x.r0 + row_of(a, c)) * a.ldq + (x.h * G + c - row_of(a, c) * G) * kHeadDim : 0) + 16 * t;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            r.w[nt][w] = in ? *reinterpret_cast<const uint4*>(q + (w & 1) * 64 + (w >> 1) * 8) : make_uint4(0, 0, 0, 0);
-    }
+    for (int w = 0; w < 4; ++w)
+        r.w[w] = in ? *reinterpret_cast<const uint4*>(q + (w & 1) * 64 + (w >> 1) * 8) : make_uint4(0, 0, 0, 0);
 }
 
 // q' by the power of two that its largest number asks for; the groups' sums by the
 // tensor cores from the same operands (ones, and 16 for the codes' high halves).
-template <int NT>
-__device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, const AttnArgs& a, const Set& x) {
+__device__ __forceinline__ void load_query(Query& q, const RawQuery& r, const AttnArgs& a, const Set& x) {
     const int lane = threadIdx.x & 31, t = lane & 3;
+    uint32_t top = 0;  // of the absolute values' bits
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        uint32_t top = 0;  // of the absolute values' bits
+    for (int w = 0; w < 4; ++w) {
+        const uint4 v = r.w[w];
+        top = __vimax3_u16x2(top, v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+        top = __vimax3_u16x2(top, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+    }
+    uint32_t m = max(top & 0xffffu, top >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int e = max(-100, min(126, 13 - ((int)(m >> 7) - 127)));
+    const float up = pow2(e), up4 = pow2(e - 4);
+    float sum[2][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint4 v = r.w[nt][w];
-            top = __vimax3_u16x2(top, v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
-            top = __vimax3_u16x2(top, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
-        }
-        uint32_t m = max(top & 0xffffu, top >> 16);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = max(-100, min(126, 13 - ((int)(m >> 7) - 127)));
-        const float up = pow2(e), up4 = pow2(e - 4);
-        float sum[2][4];
+    for (int gr = 0; gr < 2; ++gr) sum[gr][0] = sum[gr][1] = sum[gr][2] = sum[gr][3] = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) sum[gr][0] = sum[gr][1] = sum[gr][2] = sum[gr][3] = 0.f;
+    for (int w = 0; w < 4; ++w) {
+        const uint4 v = r.w[w];
+        q.b[2 * w][0] = pack_half(lo_f(v.x) * up, lo_f(v.z) * up);
+        q.b[2 * w][1] = pack_half(lo_f(v.y) * up, lo_f(v.w) * up);
+        q.b[2 * w + 1][0] = pack_half(hi_f(v.x) * up4, hi_f(v.z) * up4);
+        q.b[2 * w + 1][1] = pack_half(hi_f(v.y) * up4, hi_f(v.w) * up4);
+        mma_f16(sum[w & 1], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, q.b[2 * w][0], q.b[2 * w][1]);
+        mma_f16(sum[w & 1], 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, q.b[2 * w + 1][0],
+                q.b[2 * w + 1][1]);
+    }
+    const float f = pow2(24 - e) * kLog2eOverSqrtD;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint4 v = r.w[nt][w];
-            q.b[nt][2 * w][0] = pack_half(lo_f(v.x) * up, lo_f(v.z) * up);
-            q.b[nt][2 * w][1] = pack_half(lo_f(v.y) * up, lo_f(v.w) * up);
-            q.b[nt][2 * w + 1][0] = pack_half(hi_f(v.x) * up4, hi_f(v.z) * up4);
-            q.b[nt][2 * w + 1][1] = pack_half(hi_f(v.y) * up4, hi_f(v.w) * up4);
-            mma_f16(sum[w & 1], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, q.b[nt][2 * w][0], q.b[nt][2 * w][1]);
-            mma_f16(sum[w & 1], 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, 0x4c004c00u, q.b[nt][2 * w + 1][0],
-                    q.b[nt][2 * w + 1][1]);
-        }
-        const float f = pow2(24 - e) * kLog2eOverSqrtD;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            q.F[nt][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
-            q.Q0[nt][j] = sum[0][j] * (q.F[nt][j] * pow2(-24));
-            q.Q1[nt][j] = sum[1][j] * (q.F[nt][j] * pow2(-24));
-            const int cc = nt * 8 + 2 * t + j;
-            q.pos[nt][j] = cc < x.nc ? x.pos0 + row_of(a, x.c0 + cc) : -1;
-        }
+    for (int j = 0; j < 2; ++j) {
+        q.F[j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
+        q.Q0[j] = sum[0][j] * (q.F[j] * pow2(-24));
+        q.Q1[j] = sum[1][j] * (q.F[j] * pow2(-24));
+        const int cc = 2 * t + j;
+        q.pos[j] = cc < x.nc ? x.pos0 + row_of(a, x.c0 + cc) : -1;
     }
 }
 
@@ -511,11 +478,11 @@ __device__ __forceinline__ void load_query(Query<NT>& q, const RawQuery<NT>& r, 
 struct OutRows {
     bf16* r[2];
 };
-__device__ __forceinline__ OutRows out_rows(const AttnArgs& a, const Set& x, int G, int nt) {
+__device__ __forceinline__ OutRows out_rows(const AttnArgs& a, const Set& x, int G) {
     OutRows o;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int col = nt * 8 + 2 * (threadIdx.x & 3) + j, c = x.c0 + col, row = row_of(a, c);
+        const int col = 2 * (threadIdx.x & 3) + j, c = x.c0 + col, row = row_of(a, c);
         o.r[j] = col < x.nc ? a.out + (long)(x.r0 + row) * a.ldo + (x.h * G + c - row * G) * kHeadDim : nullptr;
     }
     return o;
@@ -541,19 +508,10 @@ struct Fetch {
     int page;                  // the unit's second page
 };
 
-template <int NT>
-struct Cfg {
-    static constexpr int kCtas = NT == 1 ? kCtas1 : 2;      // of an SM
-    static constexpr int kStages = NT == 1 ? kStages1 : 5;    // steps of a warp's ring
-    static constexpr int kBuf = kStages * (kStepBytes + 8) + 64;
-    static constexpr int kBufBytes = (kBuf + 127) / 128 * 128;
-    static constexpr int kBytes = kWarps * kBufBytes;
-};
+constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + 64 + 127) / 128 * 128;  // ring, its barriers, Fetch
 static_assert(sizeof(Fetch) <= 64, "Fetch");
 
-template <int NT>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kStages = Cfg<NT>::kStages;
+__global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_kv = a.rows.n_kv, G = a.group;
@@ -568,12 +526,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
     pdl_trigger();
     if (i >= end) return;
 
-    char* buf = smem + warp * Cfg<NT>::kBufBytes;
+    char* buf = smem + warp * kWarpBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
     Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
     Set x;
-    int u = find<NT>(a, G, i, x);
-    RawQuery<NT> raw;
+    int u = find(a, G, i, x);
+    RawQuery raw;
     ask_query(raw, a, x, G);  // before the keys, which they would wait behind
     auto open = [&](int item, const Set& y, int v) {
         const View& kv = a.rows.kv[y.s];
@@ -590,7 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
     auto open_next = [&]() {
         while (f->left == 0 && f->item + 1 < end) {
             Set y;
-            const int w = find<NT>(a, G, f->item + 1, y);
+            const int w = find(a, G, f->item + 1, y);
             open(f->item + 1, y, w);
         }
     };
@@ -601,7 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
             f->k += kStepKeys;
             f->next = f->k % kPage == 0 ? f->heads + (size_t)f->page * n_kv * kTileBytes : f->next + kStepBytes;
             --f->left;
-            if (f->left == 0) open_next();
+            open_next();
         }
         if (++fslot == kStages) fslot = 0;
     };
@@ -612,10 +570,22 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
         open_next();
     }
     __syncwarp();
+    int asked = 0;  // the first steps at once: they are contiguous (a unit begins a page, or is part of one)
+    if (lane == 0) {
+        asked = min(f->left, kStages);
+        const char* src = f->next;
+        for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
+        f->next = src;
+        f->k += asked * kStepKeys;
+        f->left -= asked;
+        open_next();
+    }
+    asked = __shfl_sync(0xffffffffu, asked, 0);
+    fslot = asked == kStages ? 0 : asked;
 #pragma unroll 1
-    for (int k = 0; k < kStages; ++k) fetch();
-    Query<NT> q;
-    State<NT> e;
+    for (int k = asked; k < kStages; ++k) fetch();
+    Query q;
+    State e;
     int slot = 0;
     uint32_t phase = 0;
     bool there = true;  // until a wait gives up, which status then says
@@ -631,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
             for (int k = k0; k < k1; k += kStepKeys) {
                 there = there && __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, a.status));
                 if (!there) continue;  // nothing more is asked for
-                step<NT, decltype(edge)::value>(e, q, buf + slot * kStepBytes, k, k == k0);
+                step<decltype(edge)::value>(e, q, buf + slot * kStepBytes, k, k == k0);
                 __syncwarp();  // the stage has been read
                 fetch();
                 if (++slot == kStages) {
@@ -646,27 +616,24 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
         else
             steps(Bool<false>());
         finish(e);
+        if (a.direct) {
+            const OutRows o = out_rows(a, x, G);
+            const float R[2] = {1.f / e.l[0], 1.f / e.l[1]};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (a.direct) {
-                const OutRows o = out_rows(a, x, G, nt);
-                const float R[2] = {1.f / e.l[nt][0], 1.f / e.l[nt][1]};
+            for (int d = 0; d < 8; ++d) put_out(o, d, f4(e.o[d]), R);
+        } else {
+            const size_t at = partial(a, x, u);
 #pragma unroll
-                for (int d = 0; d < 8; ++d) put_out(o, d, f4(e.o[nt][d]), R);
-            } else {
-                const size_t at = partial<NT>(a, x, u) + nt;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = f4(e.o[nt][d]);
-                if (lane < 4) {
-                    *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * lane) = make_float2(e.m[nt][0], e.m[nt][1]);
-                    *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(e.l[nt][0], e.l[nt][1]);
-                }
+            for (int d = 0; d < 8; ++d) reinterpret_cast<float4*>(a.po)[at * 256 + d * 32 + lane] = f4(e.o[d]);
+            if (lane < 4) {
+                *reinterpret_cast<float2*>(a.pm + at * 8 + 2 * lane) = make_float2(e.m[0], e.m[1]);
+                *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(e.l[0], e.l[1]);
             }
         }
         if (++i >= end) break;
         fresh = u + 1 == x.nu;
         if (fresh) {
-            u = find<NT>(a, G, i, x);
+            u = find(a, G, i, x);
             ask_query(raw, a, x, G);
         } else {
             ++u;
@@ -683,9 +650,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<NT>::kCtas) units_kernel(cons
 }
 
 // Joins n <= kFan partials of one tile in order, by one warp.  Partial i's eight maxima
-// and sums are at pm, pl + i * stride * 8, this lane's output at po + i * stride * 256; all
+// and sums are at pm, pl + 8 i, this lane's output at po + 256 i; all
 // loads are in flight at once.  Lane 8 a + c holds column c of partials a, a + 4, ...
-__device__ __forceinline__ void join(const float* pm, const float* pl, const float4* po, int n, int stride,
+__device__ __forceinline__ void join(const float* pm, const float* pl, const float4* po, int n,
                                      float (&M)[2], float (&L)[2], float4& O) {
     const int lane = threadIdx.x & 31, t = lane & 3, c = lane & 7, a = lane >> 3;
     constexpr int kR = kFan / 4;
@@ -694,11 +661,11 @@ __device__ __forceinline__ void join(const float* pm, const float* pl, const flo
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
         const bool in = 4 * r + a < n;
-        m[r] = in ? __ldcg(pm + (size_t)(4 * r + a) * stride * 8 + c) : kUnset;
-        l[r] = in ? __ldcg(pl + (size_t)(4 * r + a) * stride * 8 + c) : 0.f;
+        m[r] = in ? __ldcg(pm + (4 * r + a) * 8 + c) : kUnset;
+        l[r] = in ? __ldcg(pl + (4 * r + a) * 8 + c) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < kFan; ++i) v[i] = __ldcg(po + (size_t)min(i, n - 1) * stride * 256);  // past n: weight 0 below
+    for (int i = 0; i < kFan; ++i) v[i] = __ldcg(po + min(i, n - 1) * 256);  // past n: weight 0 below
     float top = m[0];
 #pragma unroll
     for (int r = 1; r < kR; ++r) top = fmaxf(top, m[r]);
@@ -723,24 +690,21 @@ __device__ __forceinline__ void join(const float* pm, const float* pl, const flo
     M[1] = __shfl_sync(0xffffffffu, top, 2 * t + 1);
 }
 
-// One tile (of a set's NT * 8) per CTA: its warps join groups of kFan units, warp 0 the
+// One tile (of a set's eight) per CTA: its warps join groups of kFan units, warp 0 the
 // groups.  A group's loads are all in flight at once, so the kernel costs about two
 // round trips to the L2, however many units.
-template <int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) float4 js[];  // [group]: 32 x float4 output, then 8 + 8 maxima and sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
     const int G = a.group;
     // the tile's set: the item of its unit 0
-    const int tile_of = blockIdx.x % (NT * 8), set = blockIdx.x / (NT * 8);
-    const int nt = tile_of >> 3, d = tile_of & 7;
+    const int d = blockIdx.x % 8, set = blockIdx.x / 8;
     int s = 0;
     while (s + 1 < a.rows.n_streams && set >= a.set_start[s + 1] * a.rows.n_kv) ++s;
     const int R = a.rows.row_start[s + 1] - a.rows.row_start[s];
     const int nu_s = (a.rows.pos0[s] + R - 1) / unit_of(a.rows.pos0[s]) + 1;
     Set x;
-    find<NT>(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
-    if (nt * 8 >= x.nc) return;  // no columns
+    find(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
     const int groups = (x.nu + kFan - 1) / kFan;
     constexpr int kGroup4 = 36;  // float4 of a group
     pdl_wait();
@@ -749,9 +713,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     float4 O;
 #pragma unroll 1
     for (int gi = warp; gi < groups; gi += blockDim.x / 32) {
-        const size_t at = partial<NT>(a, x, gi * kFan) + nt;
+        const size_t at = partial(a, x, gi * kFan);
         join(a.pm + at * 8, a.pl + at * 8, reinterpret_cast<const float4*>(a.po) + at * 256 + d * 32 + lane,
-             min(kFan, x.nu - gi * kFan), NT, M, L, O);
+             min(kFan, x.nu - gi * kFan), M, L, O);
         if (groups > 1) {
             js[gi * kGroup4 + lane] = O;
             float2* ml = reinterpret_cast<float2*>(js + gi * kGroup4 + 32);
@@ -790,7 +754,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         return;
     }
     const float inv[2] = {1.f / L[0], 1.f / L[1]};
-    put_out(out_rows(a, x, G, nt), d, O, inv);
+    put_out(out_rows(a, x, G), d, O, inv);
 }
 
 cudaLaunchConfig_t cfg(int grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
@@ -821,10 +785,8 @@ int attn_max_units(int positions) {
 }
 
 cudaError_t init_attn() {
-    cudaError_t e = allow_smem(units_kernel<1>, Cfg<1>::kBytes);
-    if (e == cudaSuccess) e = allow_smem(units_kernel<2>, Cfg<2>::kBytes);
-    if (e == cudaSuccess) e = allow_smem(join_kernel<1>, kMaxJoinBytes);
-    if (e == cudaSuccess) e = allow_smem(join_kernel<2>, kMaxJoinBytes);
+    cudaError_t e = allow_smem(units_kernel, kWarps * kWarpBytes);
+    if (e == cudaSuccess) e = allow_smem(join_kernel, kMaxJoinBytes);
     return e;
 }
 
@@ -846,14 +808,11 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     }
     const int G = a.group = a.n_q / m.n_kv;
     a.group_inv = (65536 + G - 1) / G;
-    // one tile of eight columns where every stream's rows fit it, else two: codes are then unpacked once for 16 columns
-    int nt = 1, most = 1;
-    for (int s = 0; s < m.n_streams; ++s)
-        if ((m.row_start[s + 1] - m.row_start[s]) * G > 8) nt = 2;
+    int most = 1;
     int items = 0, sets = 0;
     for (int s = 0; s < m.n_streams; ++s) {
         const int R = m.row_start[s + 1] - m.row_start[s];
-        const int chunks = (R * G + nt * 8 - 1) / (nt * 8);
+        const int chunks = (R * G + 7) / 8;
         a.item_start[s] = items;
         a.set_start[s] = sets;
         sets += chunks;
@@ -865,17 +824,17 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     }
     a.item_start[m.n_streams] = items;
     // a full grid, or as many warps as there are units
-    const int ctas = nt == 1 ? Cfg<1>::kCtas : Cfg<2>::kCtas, full = sms * ctas, need = (items + kWarps - 1) / kWarps;
-    a.per_sm = need < full ? 1 : ctas;
+    const int full = sms * kCtas, need = (items + kWarps - 1) / kWarps;
+    a.per_sm = need < full ? 1 : kCtas;
     a.direct = most == 1;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = cfg(need < full ? need : full, kWarps * 32, nt == 1 ? Cfg<1>::kBytes : Cfg<2>::kBytes, st, attr, pdl);
-    const cudaError_t e = nt == 1 ? cudaLaunchKernelEx(&c, units_kernel<1>, a) : cudaLaunchKernelEx(&c, units_kernel<2>, a);
+    cudaLaunchConfig_t c = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);
+    const cudaError_t e = cudaLaunchKernelEx(&c, units_kernel, a);
     if (e != cudaSuccess || a.direct) return e;
     const int groups = (most + kFan - 1) / kFan;
-    c = cfg(sets * m.n_kv * nt * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
+    c = cfg(sets * m.n_kv * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
             st, attr, true);
-    return nt == 1 ? cudaLaunchKernelEx(&c, join_kernel<1>, a) : cudaLaunchKernelEx(&c, join_kernel<2>, a);
+    return cudaLaunchKernelEx(&c, join_kernel, a);
 }
 
 }  // namespace kv4
