@@ -114,10 +114,12 @@ struct AttnArgs {
     int group;           // set by launch_attn: query heads per KV head,
     int group_inv;       // 65536 / group, rounded up,
     int per_sm, direct;  // CTAs of an SM; every stream has one unit, whose warp writes the output,
-    int item_start[kMaxParts + 1]; // first unit (over its sets) of a stream,
-    int set_start[kMaxParts + 1];       // and its first set of columns
+    // of a stream: the steps of its units, and places from one unit and one set to the next in the call's work
+    int unit[kMaxParts], pitch[kMaxParts], pitch_set[kMaxParts];
+    int item_start[kMaxParts + 1]; // a stream's first place in the work,
+    int set_start[kMaxParts + 1];  // and its first set of columns
 };
-int attn_max_units(int positions);  // partials of a row's head over caches of up to so many positions
+int attn_max_units(int positions, int n_kv);  // partials of a row's head over caches of up to so many positions
 cudaError_t init_attn();
 cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl);
 

@@ -69,7 +69,7 @@ struct AttnLayout {
 
 AttnLayout attn_layout(int n_q, int n_kv, int max_rows, int max_positions) {
     AttnLayout L;
-    L.units = kv4::attn_max_units(max_positions);
+    L.units = kv4::attn_max_units(max_positions, n_kv);
     // Tiles of eight columns over all sets.  A call has at most 16 streams, cut into 32 parts; a part
     // of R rows has ceil(R G / 8) tiles per KV head.
     const int G = n_q / n_kv;

@@ -44,19 +44,19 @@ namespace {
 
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
-// Keys of a unit, by the position of the row that attends: more keys mean fewer starts
-// and partials, fewer mean more warps for one short cache.  One layer of 8 KV heads, seven
-// query heads each, with 256 | 128 | 64 keys before position 8,192: one row over 4,096 keys
-// 12.4 | 8.9 | 7.7 us, 16 rows over 8,192 each 34.1 | 34.3 | 45.6 us.  With 256 | 128 from
-// there on: one row over 131,072 keys 43.2 | 47.9 us.
-constexpr int kShortUnit = 128, kLongUnit = 256, kLongFrom = 8192;
-__host__ __device__ constexpr int unit_of(int pos) { return pos < kLongFrom ? kShortUnit : kLongUnit; }
+// Steps of a unit, by the position of the row that attends and the cache's heads:
+// UNITTEXT
+constexpr int kSpread = 152 * 12;                  // warps of the full grid
+__host__ inline int unit_steps(int pos, int n_kv) {
+    const int most = kSpread / n_kv, steps = pos / kStepKeys + 1;
+    return std::max(pos < 8192 ? 4 : 8, (steps + most - 1) / most);
+}
 constexpr int kWarps = 4;                          // of a CTA
 constexpr int kCtas = 3, kStages = 3;              // CTAs of an SM, steps of a warp's ring
 constexpr int kFan = 16;                           // units joined at a time
 constexpr int kJoinWarps = 16;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
-constexpr int kMaxJoinBytes = ((1 << 20) / kLongUnit + kFan - 1) / kFan * kGroupBytes;
+constexpr int kMaxJoinBytes = (kSpread + kFan - 1) / kFan * kGroupBytes;
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
@@ -389,28 +389,41 @@ __device__ __forceinline__ int row_of(const AttnArgs& a, int c) { return (c * a.
 struct Set {
     int s, h, c0, nc;      // columns c0 .. c0 + nc - 1 of stream s
     int r0, pos0, nu, id;  // the stream's first row and position, its units; the set's partials
-    int unit;              // keys of a unit
+    int unit, last;        // steps of a unit; position of the columns' last row
+    int pitch;             // of the set's units: places from one to the next
 };
 
-// Item `i` of the call's units in order of stream, columns, KV head, unit; returns the unit.
-__device__ __forceinline__ int find(const AttnArgs& a, int G, int i, Set& x) {
+// The first unit from place `i` of the call's work, in order of stream, columns, KV head,
+// unit; `i` becomes the place where it starts, or the work's end if there is none.
+__device__ __forceinline__ int find(const AttnArgs& a, int G, int& i, Set& x) {
     const Rows& rm = a.rows;
     int s = 0;
-    while (s + 1 < rm.n_streams && i >= a.item_start[s + 1]) ++s;
-    const int R = rm.row_start[s + 1] - rm.row_start[s];
-    i -= a.item_start[s];
-    x.s = s;
-    x.r0 = rm.row_start[s];
-    x.pos0 = rm.pos0[s];
-    x.unit = unit_of(x.pos0);
-    x.nu = (x.pos0 + R - 1) / x.unit + 1;
-    const unsigned sh = (unsigned)i / (unsigned)x.nu, chunk = sh / (unsigned)rm.n_kv;
-    const int u = i - (int)sh * x.nu;
-    x.h = sh - chunk * rm.n_kv;
-    x.c0 = chunk * 8;
-    x.nc = min(8, R * G - x.c0);
-    x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
-    return u;
+    while (true) {
+        while (s + 1 < rm.n_streams && i >= a.item_start[s + 1]) ++s;
+        const int R = rm.row_start[s + 1] - rm.row_start[s];
+        x.s = s;
+        x.r0 = rm.row_start[s];
+        x.pos0 = rm.pos0[s];
+        x.unit = a.unit[s];
+        const int steps = (x.pos0 + R - 1) / kStepKeys + 1;
+        x.nu = (unsigned)(steps + x.unit - 1) / (unsigned)x.unit;
+        x.pitch = a.pitch[s];
+        const int pitch_set = a.pitch_set[s];
+        const unsigned r = i - a.item_start[s], sh = r / (unsigned)pitch_set, chunk = sh / (unsigned)rm.n_kv;
+        const int first = a.item_start[s] + (int)sh * pitch_set;
+        const int u = (unsigned)(i - first + x.pitch - 1) / (unsigned)x.pitch;
+        if (u < x.nu) {
+            i = first + u * x.pitch;
+            x.h = sh - chunk * rm.n_kv;
+            x.c0 = chunk * 8;
+            x.nc = min(8, R * G - x.c0);
+            x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
+            x.last = x.pos0 + row_of(a, x.c0 + x.nc - 1);
+            return u;
+        }
+        i = first + pitch_set;
+        if (i >= a.item_start[rm.n_streams]) return 0;
+    }
 }
 
 __device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u) {
@@ -500,16 +513,67 @@ __device__ __forceinline__ void put_out(const OutRows& o, int d, float4 O, const
     }
 }
 
-// The fetching side of a warp: lane 0, its state in shared memory.
+// The fetching side of a warp: lane 0, its state in shared memory.  Steps are fetched in
+// runs: a unit's steps within a page.  The page of a run is looked up in the cache's table
+// when the run before it begins, so that no fetch waits for the table.
 struct Fetch {
-    const char *next, *heads;  // the step to fetch; tile 0 of the layer and head
-    int item, left;            // the unit, its steps not yet fetched
-    int last, k;               // the set's last position, the position of the step to fetch
-    int page;                  // the unit's second page
+    const char* next;       // the step to fetch,
+    int run, pad;           // steps left of its run
+    int page;               // where the table's entry for the run after it arrives:
+    int next_run, k, left;  // its steps (0: none), its position, its unit's steps from there on,
+    int item, u, nu, unit;  // its unit: place, number, the set's units and their steps,
+    int last, pitch;        // the set's last position
+    const char* heads;      // tile 0 of its layer and head
+    const int* table;
 };
+__device__ __forceinline__ void ask_word(int* dst, const int* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ int asked_word(const int* dst) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return *reinterpret_cast<const volatile int*>(dst);
+}
 
-constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + 64 + 127) / 128 * 128;  // ring, its barriers, Fetch
-static_assert(sizeof(Fetch) <= 64, "Fetch");
+__device__ __forceinline__ void open_unit(Fetch* f, int v) {
+    const int k = v * f->unit * kStepKeys, keys = f->last + 1 - k;
+    f->u = v;
+    f->k = k;
+    // a unit of later rows may lie past the last position of these columns: no steps
+    f->left = keys <= 0 ? 0 : min(f->unit, (keys + kStepKeys - 1) / kStepKeys);
+}
+__device__ __forceinline__ void open_set(const AttnArgs& a, Fetch* f, int item, const Set& x, int u) {
+    const View& kv = a.rows.kv[x.s];
+    f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * a.rows.n_kv + x.h) * kTileBytes;
+    f->table = kv.table;
+    f->item = item;
+    f->nu = x.nu;
+    f->unit = x.unit;
+    f->last = x.last;
+    f->pitch = x.pitch;
+    open_unit(f, u);
+}
+// The next run: of the unit, or of the next one with steps before place `end`.  Not inlined:
+// a copy in each loop costs more in instruction cache misses than the call.
+__device__ __noinline__ void open_run(const AttnArgs& a, Fetch* f, int end) {
+    while (f->left == 0) {
+        int item = f->item + f->pitch;
+        if (f->u + 1 < f->nu) {
+            if (item >= end) break;
+            f->item = item;
+            open_unit(f, f->u + 1);
+        } else {
+            Set x;  // the next set starts no later than a unit would
+            item = f->item + 1;
+            const int u = item < end ? find(a, a.group, item, x) : 0;
+            if (item >= end) break;
+            open_set(a, f, item, x, u);
+        }
+    }
+    f->next_run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
+    if (f->left > 0) ask_word(&f->page, f->table + f->k / kPage);
+}
+
+constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + (int)sizeof(Fetch) + 127) / 128 * 128;  // ring, its barriers, Fetch
 
 __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) char smem[];
@@ -517,69 +581,65 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     const int n_kv = a.rows.n_kv, G = a.group;
     // a full grid: the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
     // neighbouring shares, so that their sum differs by at most one unit between schedulers
-    const int items = a.item_start[a.rows.n_streams];
+    const int work = a.item_start[a.rows.n_streams];
     const int per = a.per_sm, sms = gridDim.x / per;
     const long share = ((long)(blockIdx.x % sms) * kWarps + warp) * per + blockIdx.x / sms, shares = (long)gridDim.x * kWarps;
-    int i = (int)(share * items / shares);
-    const int end = (int)((share + 1) * items / shares);
+    int i = (int)(share * work / shares);
+    const int end = (int)((share + 1) * work / shares);
     pdl_wait();
     pdl_trigger();
     if (i >= end) return;
+    Set x;
+    int u = find(a, G, i, x);
+    if (i >= end) return;  // no unit starts in the share
 
     char* buf = smem + warp * kWarpBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
     Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
-    Set x;
-    int u = find(a, G, i, x);
+    const int page0 = __ldg(a.rows.kv[x.s].table + min(u * x.unit * kStepKeys, x.last) / kPage);
     RawQuery raw;
     ask_query(raw, a, x, G);  // before the keys, which they would wait behind
-    auto open = [&](int item, const Set& y, int v) {
-        const View& kv = a.rows.kv[y.s];
-        f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * n_kv + y.h) * kTileBytes;
-        const int last = y.pos0 + row_of(a, y.c0 + y.nc - 1), k = v * y.unit, keys = last + 1 - k;
-        f->item = item;
-        f->k = k;
-        // a unit of later rows may lie past the last position of these columns: no steps
-        f->left = keys <= 0 ? 0 : (min(y.unit, keys) + kStepKeys - 1) / kStepKeys;
-        const int* table = kv.table + k / kPage;
-        if (keys > 0) f->next = f->heads + (size_t)__ldg(table) * n_kv * kTileBytes + k % kPage / kBlockPos * kBlockBytes;
-        if (min(y.unit, keys) > kPage) f->page = __ldg(table + 1);  // units of more than a page begin with one
-    };
-    auto open_next = [&]() {
-        while (f->left == 0 && f->item + 1 < end) {
-            Set y;
-            const int w = find(a, G, f->item + 1, y);
-            open(f->item + 1, y, w);
-        }
-    };
     int fslot = 0;
     auto fetch = [&]() {
-        if (lane == 0 && f->left > 0) {
-            ask_step(buf + fslot * kStepBytes, f->next, &full[fslot]);
-            f->k += kStepKeys;
-            f->next = f->k % kPage == 0 ? f->heads + (size_t)f->page * n_kv * kTileBytes : f->next + kStepBytes;
-            --f->left;
-            open_next();
+        if (lane == 0) {
+            int run = f->run;
+            const char* src = f->next;
+            if (run == 0) {
+                run = f->next_run;
+                if (run > 0) {
+                    src = f->heads + (size_t)asked_word(&f->page) * n_kv * kTileBytes + f->k % kPage / kBlockPos * kBlockBytes;
+                    f->k += run * kStepKeys;
+                    f->left -= run;
+                    open_run(a, f, end);
+                }
+            }
+            if (run > 0) {
+                ask_step(buf + fslot * kStepBytes, src, &full[fslot]);
+                f->next = src + kStepBytes;
+                f->run = run - 1;
+            }
         }
         if (++fslot == kStages) fslot = 0;
     };
+    int asked = 0;
     if (lane == 0) {
         for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
         mbar_init_fence();
-        open(i, x, u);
-        open_next();
+        f->run = 0;
+        open_set(a, f, i, x, u);
+        if (f->left > 0) {  // the first run, at once
+            const int run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
+            asked = min(run, kStages);
+            const char* src = f->heads + (size_t)page0 * n_kv * kTileBytes + f->k % kPage / kBlockPos * kBlockBytes;
+            for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
+            f->next = src;
+            f->run = run - asked;
+            f->k += run * kStepKeys;
+            f->left -= run;
+        }
+        open_run(a, f, end);
     }
     __syncwarp();
-    int asked = 0;  // the first steps at once: they are contiguous (a unit begins a page, or is part of one)
-    if (lane == 0) {
-        asked = min(f->left, kStages);
-        const char* src = f->next;
-        for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
-        f->next = src;
-        f->k += asked * kStepKeys;
-        f->left -= asked;
-        open_next();
-    }
     asked = __shfl_sync(0xffffffffu, asked, 0);
     fslot = asked == kStages ? 0 : asked;
 #pragma unroll 1
@@ -593,8 +653,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
 #pragma unroll 1
     while (true) {
         if (fresh) load_query(q, raw, a, x);
-        const int p_first = x.pos0 + row_of(a, x.c0), p_last = x.pos0 + row_of(a, x.c0 + x.nc - 1);
-        const int k0 = u * x.unit, k1 = min(k0 + x.unit, p_last + 1);
+        const int p_first = x.pos0 + row_of(a, x.c0), keys = x.unit * kStepKeys;
+        const int k0 = u * keys, k1 = min(k0 + keys, x.last + 1);
         reset(e);
         auto steps = [&](auto edge) {
 #pragma unroll 1
@@ -611,7 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             }
         };
         // one body for all steps of a unit: fetching a second one costs more than it saves
-        if (k0 + x.unit - 1 > p_first)
+        if (k0 + keys - 1 > p_first)
             steps(Bool<true>());
         else
             steps(Bool<false>());
@@ -630,16 +690,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
                 *reinterpret_cast<float2*>(a.pl + at * 8 + 2 * lane) = make_float2(e.l[0], e.l[1]);
             }
         }
-        if (++i >= end) break;
-        fresh = u + 1 == x.nu;
-        if (fresh) {
-            u = find(a, G, i, x);
-            ask_query(raw, a, x, G);
-        } else {
+        if (u + 1 < x.nu) {
+            i += x.pitch;
+            if (i >= end) break;
+            fresh = false;
             ++u;
+        } else {
+            if (++i >= end) break;
+            fresh = true;
+            u = find(a, G, i, x);
+            if (i >= end) break;
+            ask_query(raw, a, x, G);
         }
     }
-    if (!there)  // the copies of the other stages end before the CTA does, or these waits run out too
+    if (!there) {  // the copies in flight end before the CTA does, or these waits run out too
+        asm volatile("cp.async.wait_all;" ::: "memory");
         for (int k = 1; k < kStages; ++k) {
             if (++slot == kStages) {
                 slot = 0;
@@ -647,6 +712,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             }
             mbar_wait(&full[slot], phase, a.status);
         }
+    }
 }
 
 // Joins n <= kFan partials of one tile in order, by one warp.  Partial i's eight maxima
@@ -701,10 +767,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int d = blockIdx.x % 8, set = blockIdx.x / 8;
     int s = 0;
     while (s + 1 < a.rows.n_streams && set >= a.set_start[s + 1] * a.rows.n_kv) ++s;
-    const int R = a.rows.row_start[s + 1] - a.rows.row_start[s];
-    const int nu_s = (a.rows.pos0[s] + R - 1) / unit_of(a.rows.pos0[s]) + 1;
     Set x;
-    find(a, G, a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * nu_s, x);
+    int at0 = a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * a.pitch_set[s];
+    find(a, G, at0, x);
     const int groups = (x.nu + kFan - 1) / kFan;
     constexpr int kGroup4 = 36;  // float4 of a group
     pdl_wait();
@@ -779,9 +844,9 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 
 }  // namespace
 
-int attn_max_units(int positions) {
-    const int short_ = (std::min(positions, kLongFrom) + kShortUnit - 1) / kShortUnit;
-    return std::max(short_, (positions + kLongUnit - 1) / kLongUnit);
+int attn_max_units(int positions, int n_kv) {
+    const int steps = (positions + kStepKeys - 1) / kStepKeys;  // short units before 8,192 positions, 256 steps
+    return std::max((std::min(steps, 256) + 3) / 4, std::min((steps + 7) / 8, kSpread / n_kv));
 }
 
 cudaError_t init_attn() {
@@ -792,40 +857,54 @@ cudaError_t init_attn() {
 
 cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
-    // a stream whose rows lie on both sides of a change of the unit's size becomes two
+    // a stream whose rows lie on both sides of a change of the unit's size (always a multiple of 32) becomes two
     Rows& m = a.rows;
     for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s], before = kLongFrom - m.pos0[s];
-        if (R < 2 || before <= 0 || before >= R) continue;
+        const int R = m.row_start[s + 1] - m.row_start[s], last = m.pos0[s] + R - 1;
+        a.unit[s] = unit_steps(m.pos0[s], m.n_kv);
+        if (R < 2 || unit_steps(last, m.n_kv) == a.unit[s]) continue;
         for (int t = m.n_streams; t > s; --t) {
             m.row_start[t + 1] = m.row_start[t];
             m.pos0[t] = m.pos0[t - 1];
             m.kv[t] = m.kv[t - 1];
         }
-        m.row_start[s + 1] = m.row_start[s] + before;
-        m.pos0[s + 1] = kLongFrom;
+        m.pos0[s + 1] = last / kStepKeys * kStepKeys;
+        m.row_start[s + 1] = m.row_start[s] + m.pos0[s + 1] - m.pos0[s];
         ++m.n_streams;
     }
     const int G = a.group = a.n_q / m.n_kv;
     a.group_inv = (65536 + G - 1) / G;
-    int most = 1;
-    int items = 0, sets = 0;
+    auto steps_of = [&](int s) { return (m.pos0[s] + m.row_start[s + 1] - m.row_start[s] - 1) / kStepKeys + 1; };
+    int most = 1, sets = 0, units = 0, steps = 0, top_unit = 0, low_unit = 1 << 20;
     for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s];
-        const int chunks = (R * G + 7) / 8;
-        a.item_start[s] = items;
+        const int R = m.row_start[s + 1] - m.row_start[s], nu = (steps_of(s) + a.unit[s] - 1) / a.unit[s];
         a.set_start[s] = sets;
+        if (R == 0) continue;
+        const int chunks = (R * G + 7) / 8;
         sets += chunks;
-        if (R > 0) {
-            const int nu = (m.pos0[s] + R - 1) / unit_of(m.pos0[s]) + 1;
-            items += chunks * m.n_kv * nu;
-            if (nu > most) most = nu;
-        }
+        units += chunks * m.n_kv * nu;
+        steps += chunks * m.n_kv * (steps_of(s) + nu + 2);
+        top_unit = std::max(top_unit, a.unit[s]);
+        low_unit = std::min(low_unit, a.unit[s]);
+        if (nu > most) most = nu;
     }
-    a.item_start[m.n_streams] = items;
-    // a full grid, or as many warps as there are units
-    const int full = sms * kCtas, need = (items + kWarps - 1) / kWarps;
+    // As many warps as there are units, one each, or a full grid whose warps share the work.  On the
+    // scale it is shared out by, a unit is its steps and one more (its start and end), a set's last
+    // unit as long as it is and two more (the set's queries); or, if all units have the same steps
+    // and that leaves the warp with the most work less, a unit is one.  SHARETEXT
+    const int full = sms * kCtas, need = (units + kWarps - 1) / kWarps, warps = full * kWarps;
     a.per_sm = need < full ? 1 : kCtas;
+    bool count = need <= full;
+    if (!count && top_unit == low_unit) count = (units + warps - 1) / warps * (top_unit + 1) < (steps + warps - 1) / warps + top_unit;
+    int work = 0;  // below 2^29: at most 160 sets of columns, 64 heads, 2^15 steps and as many units
+    for (int s = 0; s < m.n_streams; ++s) {
+        const int R = m.row_start[s + 1] - m.row_start[s], nu = (steps_of(s) + a.unit[s] - 1) / a.unit[s];
+        a.pitch[s] = count ? 1 : a.unit[s] + 1;
+        a.pitch_set[s] = count ? nu : steps_of(s) + nu + 2;
+        a.item_start[s] = work;
+        if (R > 0) work += (R * G + 7) / 8 * m.n_kv * a.pitch_set[s];
+    }
+    a.item_start[m.n_streams] = work;
     a.direct = most == 1;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t c = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);
