@@ -53,8 +53,8 @@ __host__ inline int unit_steps(int pos, int n_kv) {
 }
 constexpr int kWarps = 4;                          // of a CTA
 constexpr int kCtas = 3, kStages = 3;              // CTAs of an SM, steps of a warp's ring
-constexpr int kFan = 16;                           // units joined at a time
-constexpr int kJoinWarps = 16;
+constexpr int kFan = 8;                            // units joined at a time
+constexpr int kJoinWarps = 16, kManyJoinWarps = 4;  // of a CTA: on a grid of at most a CTA per SM, or more
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
 constexpr int kMaxJoinBytes = (kSpread + kFan - 1) / kFan * kGroupBytes;
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
@@ -911,7 +911,7 @@ cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     const cudaError_t e = cudaLaunchKernelEx(&c, units_kernel, a);
     if (e != cudaSuccess || a.direct) return e;
     const int groups = (most + kFan - 1) / kFan;
-    c = cfg(sets * m.n_kv * 8, (groups < kJoinWarps ? groups : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
+    c = cfg(sets * m.n_kv * 8, std::min(groups, sets * m.n_kv * 8 > sms ? kManyJoinWarps : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
             st, attr, true);
     return cudaLaunchKernelEx(&c, join_kernel, a);
 }
