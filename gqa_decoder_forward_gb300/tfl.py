@@ -112,15 +112,16 @@ SIGNATURES = {
     "tfl_kv4_reset": (ctypes.c_int, [_vp, ctypes.c_int]),
     "tfl_kv4_length": (ctypes.c_int, [_vp]),
     "tfl_kv4_capacity": (ctypes.c_int, [_vp]),
-    "tfl_kv4_write": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp, _vp,
+    # arrays as addresses, which cost less per call than typed pointers (see KV4Rows)
+    "tfl_kv4_write": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
                                      ctypes.c_size_t, _vp]),
-    "tfl_kv4_read": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp, _vp,
+    "tfl_kv4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
                                     ctypes.c_size_t, _vp]),
     "tfl_kv4_attn_bytes": (ctypes.c_size_t, [ctypes.c_int] * 5),
     "tfl_kv4_attn_init": (ctypes.c_int, [ctypes.c_int] * 5 + [_vp, ctypes.c_size_t, ctypes.POINTER(_vp)]),
     "tfl_kv4_attn_free": (None, [_vp]),
     "tfl_kv4_attn_status": (ctypes.c_int, [_vp, _vp]),
-    "tfl_kv4_attention": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _intp, _intp, _vp,
+    "tfl_kv4_attention": (ctypes.c_int, [_vp, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
                                          ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
     "tfl_kv4_step_workspace_bytes": (ctypes.c_size_t, [_vp]),
     "tfl_decode_step_kv4": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_vp), ctypes.c_int, _vp, _intp, _vp, _vp,
@@ -530,6 +531,7 @@ class KV4Rows:
         self.handles = (_vp * self.n)(*[kv.handle for kv in self.kvs])
         self.pos0 = (ctypes.c_int * self.n)()
         self.rows = (ctypes.c_int * self.n)()
+        self.handles_at, self.pos0_at, self.rows_at = map(ctypes.addressof, (self.handles, self.pos0, self.rows))
         self.set(pos0, rows)
 
     def set(self, pos0: Sequence[int], rows: Sequence[int]):
@@ -567,9 +569,9 @@ def tfl_kv4_attn_status(attn: KV4Attention, stream=None) -> int:
 def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:
     """Row stride (elements) of a bf16 CUDA tensor of at least n rows of heads x 128
     numbers, [rows, heads, 128] or [rows, heads * 128]; only rows may be strided."""
-    sh, st = t.shape, t.stride()
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise ValueError("expected a bf16 CUDA tensor")
+    sh, st = t.shape, t.stride()
     if len(sh) == 2:
         ok = sh[1] == heads * 128 and st[1] == 1
     else:
@@ -582,7 +584,7 @@ def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:
 def _stream_of(t: torch.Tensor, stream) -> int:
     """The stream to enqueue on: torch's current one of the tensor's device if none is given (looked up without
     making a Stream object, which would cost as much as a launch)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
 def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -590,7 +592,7 @@ def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, 
     ld = _rows_arg(k, batch.total, batch.n_kv)
     if _rows_arg(v, batch.total, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
-    return _check(lib().tfl_kv4_write(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
+    return _check(lib().tfl_kv4_write(batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at, k.data_ptr(),
                                       v.data_ptr(), ld, _stream_of(k, stream)))
 
 
@@ -599,7 +601,7 @@ def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, s
     ld = _rows_arg(k, batch.total, batch.n_kv)
     if _rows_arg(v, batch.total, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
-    return _check(lib().tfl_kv4_read(batch.handles, batch.n, layer, batch.pos0, batch.rows, k.data_ptr(),
+    return _check(lib().tfl_kv4_read(batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at, k.data_ptr(),
                                      v.data_ptr(), ld, _stream_of(k, stream)))
 
 
@@ -608,7 +610,7 @@ def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.T
     """Attention of the rows q over the caches of batch (which hold those rows' own keys and values)."""
     ldq = _rows_arg(q, batch.total, attn.n_q)
     ldo = _rows_arg(out, batch.total, attn.n_q)
-    return _check(lib().tfl_kv4_attention(attn.handle, batch.handles, batch.n, layer, batch.pos0, batch.rows,
+    return _check(lib().tfl_kv4_attention(attn.handle, batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at,
                                           q.data_ptr(), ldq, out.data_ptr(), ldo, _stream_of(q, stream)))
 
 
