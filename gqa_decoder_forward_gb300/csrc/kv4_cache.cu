@@ -3,9 +3,9 @@
 // numbers against 72 held), so a lane moves 16 dense bytes at a time and keeps
 // several rows in flight.
 //
-// Write: sixteen lanes take one (row, head) of keys or values: a lane loads eight
-// bf16 numbers, eight lanes find their group's minimum and maximum by shuffles, and
-// each lane writes one 32-bit word of codes.
+// Write: sixteen lanes take one (row, head): a lane loads eight bf16 numbers of the key
+// and of the value, eight lanes find their group's minimum and maximum by shuffles,
+// and each lane writes one 32-bit word of codes of either.
 // Read: a warp takes 16 positions of a block (1,152 contiguous bytes of the cache,
 // half a block), a half warp a row at a time; a lane holds one word of eight rows.
 #include "kv4.cuh"
@@ -16,26 +16,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kItems = kThreads / 16;  // (row, head) items of a CTA
-constexpr float kRound = 12582912.f;   // 1.5 * 2^23
+constexpr float kRound = 12582912.f;   // 1.5 * 2^23, in bits 0x4b400000
+constexpr uint32_t kRoundCodes = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8);  // (<< 12 and more: 0)
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    const int kind = blockIdx.y;
-    const long item = (long)blockIdx.x * kItems + threadIdx.x / 16;
+// Eight numbers x8 (loaded: raw) of a row to the half block hb.  All lanes of the warp call it.
+__device__ __forceinline__ void write8(const bf16* x8, const uint4& raw, char* hb, int pos, bool live) {
     const int lane = threadIdx.x & 15;
-    const long n_items = (long)a.rows.n_rows * a.rows.n_kv;
-    const bool live = item < n_items;  // whole half-warps; the others take part in the shuffles
-    const long it = live ? item : n_items - 1;
-    const int r = (int)(it / a.rows.n_kv), h = (int)(it % a.rows.n_kv);
-    const int s = stream_of(a.rows, r);
-    const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
-    const long src = a.wrap ? 2l * kPage * s + pos % kPage : r;
-    const bf16* x8 = (kind ? a.v : a.k) + src * a.ld + (long)h * kHeadDim + lane * 8;
-    const uint4 raw = *reinterpret_cast<const uint4*>(x8);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float f[8];
 #pragma unroll
@@ -43,23 +32,17 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         f[2 * i] = lo_f(w[i]);
         f[2 * i + 1] = hi_f(w[i]);
     }
-    float mn = f[0], mx = f[0];
-    bool bad = false;
+    // (maximum, -minimum) of the group, two bf16 numbers in a word; a NaN stays one
+    auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    auto u2 = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+    auto most = [&](uint32_t x, uint32_t y) { return u2(__hmax2_nan(b2(x), b2(y))); };
+    const uint32_t hi = most(most(w[0], w[1]), most(w[2], w[3]));
+    const uint32_t lo = u2(__hmin2_nan(__hmin2_nan(b2(w[0]), b2(w[1])), __hmin2_nan(b2(w[2]), b2(w[3])))) ^ 0x80008000u;
+    uint32_t m = most(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mn = fminf(mn, f[i]);
-        mx = fmaxf(mx, f[i]);
-        bad |= !(fabsf(f[i]) < INFINITY);
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    const unsigned bads = __ballot_sync(0xffffffffu, bad);
-    bad = ((bads >> (threadIdx.x & 24)) & 0xffu) != 0;  // of this lane's eight
-    const float span = mx - mn;
-    bad |= !(span < INFINITY);
+    for (int o = 1; o < 8; o <<= 1) m = most(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mn = -hi_f(m), span = lo_f(m) - mn;
+    const bool bad = !(span < INFINITY);  // a NaN or an infinity in the group, or too wide
     const bf16 scale = rn(span / 15.f);
     const float sc = bf(scale);
     uint32_t code = 0;
@@ -67,14 +50,15 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         // n = round_half_even((x - zero) / scale) by the reciprocal, as the low bits of 1.5 2^23 + n.  The
         // quotient's error, 2^-21 of at most 16, can only change n within 2^-17 of a half: there, and for
         // scales whose reciprocal overflows or that are so coarse that n could pass 15, the lane divides.
-        const float r = 1.f / sc;
+        const float r = __fdividef(1.f, sc);  // 0 where it overflows or nearly does
         bool near = !(sc >= 1.17549435e-38f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float d = f[i] - mn, u = fmaf(d, r, kRound), rest = fmaf(kRound - u, sc, d);
             near |= !(fabsf(rest) < 0.4999f * sc);
-            code |= (__float_as_uint(u) & 15u) << (4 * i);
+            code += __float_as_uint(u) << (4 * i);  // 0x4b400000 + n, whose sum comes off below
         }
+        code -= kRoundCodes;
         if (near) {
             code = 0;
 #pragma unroll 1
@@ -86,7 +70,6 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         }
     }
     if (live) {
-        char* hb = half_block(tile(a.rows.kv[s], a.rows.layer, a.rows.n_kv, pos, h), pos, kind);
         *reinterpret_cast<uint32_t*>(hb + word_at(pos, lane & 7, lane >> 3)) = code;
         if ((lane & 7) == 0) {
             const uint32_t sb = bad ? 0u : (uint32_t)__bfloat16_as_ushort(scale);
@@ -95,6 +78,23 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
                 sb | (zb << 16);
         }
     }
+}
+
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const unsigned n_kv = a.rows.n_kv, n_items = (unsigned)a.rows.n_rows * n_kv;  // at most 2^30
+    const unsigned item = blockIdx.x * kItems + threadIdx.x / 16, it = min(item, n_items - 1);
+    const int lane = threadIdx.x & 15;
+    const bool live = item < n_items;  // whole half-warps; the others take part in the shuffles
+    const int r = (int)(it / n_kv), h = (int)(it - r * n_kv);
+    const int s = stream_of(a.rows, r);
+    const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
+    const int kind = blockIdx.y;
+    const long src = (a.wrap ? 2l * kPage * s + pos % kPage : r) * a.ld + (long)h * kHeadDim + lane * 8;
+    const bf16* x8 = (kind ? a.v : a.k) + src;
+    const uint4 raw = *reinterpret_cast<const uint4*>(x8);
+    write8(x8, raw, half_block(tile(a.rows.kv[s], a.rows.layer, a.rows.n_kv, pos, h), pos, kind), pos, live);
 }
 
 // Two bf16 numbers, each z + s n rounded once to fp32 and then to bf16.
