@@ -48,17 +48,15 @@ struct View {
 };
 
 // Rows of one call, grouped by stream: rows [row_start[s], row_start[s+1])
-// belong to stream s and sit at positions pos0[s], pos0[s]+1, ...  (Attention may cut
-// a call's streams in two: room for twice as many.)
-constexpr int kMaxParts = 2 * kMaxStreams;
+// belong to stream s and sit at positions pos0[s], pos0[s]+1, ...
 struct Rows {
     int n_streams;
     int n_rows;
     int n_kv;
     int layer;
-    int row_start[kMaxParts + 1];
-    int pos0[kMaxParts];
-    View kv[kMaxParts];
+    int row_start[kMaxStreams + 1];
+    int pos0[kMaxStreams];
+    View kv[kMaxStreams];
 };
 
 __device__ __forceinline__ int stream_of(const Rows& m, int r) {
@@ -106,22 +104,16 @@ struct AttnArgs {
     long ldq;
     bf16* out;
     long ldo;
-    // partials of (stream, columns, KV head) "sets", per unit: maxima and sums
-    // [set][unit][column of the set's tiles], outputs [set][unit][tile][8][lane] of float4 (kv4_attn.cu)
+    // partials of (part, columns, KV head) "sets", per unit: maxima and sums
+    // [set][unit][column], outputs [set][unit][tile][lane] of float4 (kv4_attn.cu)
     float *pm, *pl, *po;
     int max_units;
     int* status;         // device status word: a bounded wait that gives up raises kStatusDevice
-    int group;           // set by launch_attn: query heads per KV head,
-    int group_inv;       // 65536 / group, rounded up,
-    int per_sm, direct;  // CTAs of an SM; every stream has one unit, whose warp writes the output,
-    // of a stream: the steps of its units, and places from one unit and one set to the next in the call's work
-    int unit[kMaxParts], pitch[kMaxParts], pitch_set[kMaxParts];
-    int item_start[kMaxParts + 1]; // a stream's first place in the work,
-    int set_start[kMaxParts + 1];  // and its first set of columns
 };
+constexpr int kMaxParts = 2 * kMaxStreams;  // attention may cut a call's streams in two
 int attn_max_units(int positions, int n_kv);  // partials of a row's head over caches of up to so many positions
 cudaError_t init_attn();
-cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl);
+cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl);
 
 }  // namespace kv4
 }  // namespace tfl

@@ -382,51 +382,73 @@ struct Bool {
 
 __device__ __forceinline__ float4 f4(const float (&o)[4]) { return make_float4(o[0], o[1], o[2], o[3]); }
 
-// c / (query heads per KV head), c below 4,096.
-__device__ __forceinline__ int row_of(const AttnArgs& a, int c) { return (c * a.group_inv) >> 16; }
-
-// What a (stream, KV head, columns) set of a call is.
-struct Set {
-    int s, h, c0, nc;      // columns c0 .. c0 + nc - 1 of stream s
-    int r0, pos0, nu, id;  // the stream's first row and position, its units; the set's partials
-    int unit, last;        // steps of a unit; position of the columns' last row
-    int pitch;             // of the set's units: places from one to the next
+// What the kernels are told.  A part is a stream's rows whose units have the same length; its
+// work is a row of places, pitch_set for a set of (columns, KV head), pitch for a unit.  What a
+// warp needs of a part is together, so that it costs few misses of the constant cache.
+struct Part {
+    const char* heads;             // tile 0 of the layer
+    const int* table;
+    size_t page_bytes;             // of the layer: n_kv tiles
+    int row0, pos0, rows;
+    int unit, nu;                  // steps of a unit, units of a set
+    int pitch, pitch_set, set0;    // set0: sets of columns before the part
+};
+struct Call {
+    int n_parts, n_kv, group, group_inv;  // query heads per KV head; 65536 / group, rounded up
+    int per_sm, direct, max_units;        // CTAs of an SM; every set has one unit, whose warp writes the output
+    int end;                              // places of the call
+    const bf16* q;
+    long ldq;
+    bf16* out;
+    long ldo;
+    float *pm, *pl, *po;
+    int* status;
+    int start[kMaxParts];                 // a part's first place
+    Part part[kMaxParts];
 };
 
-// The first unit from place `i` of the call's work, in order of stream, columns, KV head,
-// unit; `i` becomes the place where it starts, or the work's end if there is none.
-__device__ __forceinline__ int find(const AttnArgs& a, int G, int& i, Set& x) {
-    const Rows& rm = a.rows;
-    int s = 0;
+// c / (query heads per KV head), c below 4,096.
+__device__ __forceinline__ int row_of(const Call& a, int c) { return (c * a.group_inv) >> 16; }
+
+// A (part, KV head, columns) set of a call.
+struct Set {
+    int p, h, c0, nc;      // columns c0 .. c0 + nc - 1 of part p
+    int r0, pos0, nu, id;  // the part's first row and position, its units; the set's partials
+    int unit, last;        // steps of a unit; position of the columns' last row
+    int pitch;
+};
+
+// The first unit from place `i` on, in order of part, columns, KV head, unit; `i` becomes
+// the place where it starts, or the call's end if there is none.
+__device__ __forceinline__ int find(const Call& a, int& i, Set& x) {
+    int p = 0;
     while (true) {
-        while (s + 1 < rm.n_streams && i >= a.item_start[s + 1]) ++s;
-        const int R = rm.row_start[s + 1] - rm.row_start[s];
-        x.s = s;
-        x.r0 = rm.row_start[s];
-        x.pos0 = rm.pos0[s];
-        x.unit = a.unit[s];
-        const int steps = (x.pos0 + R - 1) / kStepKeys + 1;
-        x.nu = (unsigned)(steps + x.unit - 1) / (unsigned)x.unit;
-        x.pitch = a.pitch[s];
-        const int pitch_set = a.pitch_set[s];
-        const unsigned r = i - a.item_start[s], sh = r / (unsigned)pitch_set, chunk = sh / (unsigned)rm.n_kv;
-        const int first = a.item_start[s] + (int)sh * pitch_set;
-        const int u = (unsigned)(i - first + x.pitch - 1) / (unsigned)x.pitch;
+        while (p + 1 < a.n_parts && i >= a.start[p + 1]) ++p;
+        const Part& q = a.part[p];
+        x.p = p;
+        x.r0 = q.row0;
+        x.pos0 = q.pos0;
+        x.unit = q.unit;
+        x.nu = q.nu;
+        x.pitch = q.pitch;
+        const unsigned r = i - a.start[p], sh = r / (unsigned)q.pitch_set, chunk = sh / (unsigned)a.n_kv;
+        const int first = a.start[p] + (int)sh * q.pitch_set;
+        const int u = (unsigned)(i - first + q.pitch - 1) / (unsigned)q.pitch;
         if (u < x.nu) {
-            i = first + u * x.pitch;
-            x.h = sh - chunk * rm.n_kv;
+            i = first + u * q.pitch;
+            x.h = sh - chunk * a.n_kv;
             x.c0 = chunk * 8;
-            x.nc = min(8, R * G - x.c0);
-            x.id = (a.set_start[s] + chunk) * rm.n_kv + x.h;
+            x.nc = min(8, q.rows * a.group - x.c0);
+            x.id = (q.set0 + chunk) * a.n_kv + x.h;
             x.last = x.pos0 + row_of(a, x.c0 + x.nc - 1);
             return u;
         }
-        i = first + pitch_set;
-        if (i >= a.item_start[rm.n_streams]) return 0;
+        i = first + q.pitch_set;
+        if (i >= a.end) return 0;
     }
 }
 
-__device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u) {
+__device__ __forceinline__ size_t partial(const Call& a, const Set& x, int u) {
     return (size_t)x.id * a.max_units + u;
 }
 
@@ -436,9 +458,9 @@ __device__ __forceinline__ size_t partial(const AttnArgs& a, const Set& x, int u
 struct RawQuery {
     uint4 w[4];
 };
-__device__ __forceinline__ void ask_query(RawQuery& r, const AttnArgs& a, const Set& x, int G) {
+__device__ __forceinline__ void ask_query(RawQuery& r, const Call& a, const Set& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int c = x.c0 + g;
+    const int c = x.c0 + g, G = a.group;
     const bool in = g < x.nc;
     const bf16* q = a.q + (in ? (long)(x.r0 + row_of(a, c)) * a.ldq + (x.h * G + c - row_of(a, c) * G) * kHeadDim : 0) + 16 * t;
 #pragma unroll
@@ -448,7 +470,7 @@ __device__ __forceinline__ void ask_query(RawQuery& r, const AttnArgs& a, const 
 
 // q' by the power of two that its largest number asks for; the groups' sums by the
 // tensor cores from the same operands (ones, and 16 for the codes' high halves).
-__device__ __forceinline__ void load_query(Query& q, const RawQuery& r, const AttnArgs& a, const Set& x) {
+__device__ __forceinline__ void load_query(Query& q, const RawQuery& r, const Call& a, const Set& x) {
     const int lane = threadIdx.x & 31, t = lane & 3;
     uint32_t top = 0;  // of the absolute values' bits
 #pragma unroll
@@ -491,7 +513,8 @@ __device__ __forceinline__ void load_query(Query& q, const RawQuery& r, const At
 struct OutRows {
     bf16* r[2];
 };
-__device__ __forceinline__ OutRows out_rows(const AttnArgs& a, const Set& x, int G) {
+__device__ __forceinline__ OutRows out_rows(const Call& a, const Set& x) {
+    const int G = a.group;
     OutRows o;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -525,6 +548,7 @@ struct Fetch {
     int last, pitch;        // the set's last position
     const char* heads;      // tile 0 of its layer and head
     const int* table;
+    size_t page_bytes;
 };
 __device__ __forceinline__ void ask_word(int* dst, const int* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -541,10 +565,11 @@ __device__ __forceinline__ void open_unit(Fetch* f, int v) {
     // a unit of later rows may lie past the last position of these columns: no steps
     f->left = keys <= 0 ? 0 : min(f->unit, (keys + kStepKeys - 1) / kStepKeys);
 }
-__device__ __forceinline__ void open_set(const AttnArgs& a, Fetch* f, int item, const Set& x, int u) {
-    const View& kv = a.rows.kv[x.s];
-    f->heads = kv.pages + ((size_t)a.rows.layer * kv.n_pages * a.rows.n_kv + x.h) * kTileBytes;
-    f->table = kv.table;
+__device__ __forceinline__ void open_set(const Call& a, Fetch* f, int item, const Set& x, int u) {
+    const Part& p = a.part[x.p];
+    f->heads = p.heads + x.h * kTileBytes;
+    f->table = p.table;
+    f->page_bytes = p.page_bytes;
     f->item = item;
     f->nu = x.nu;
     f->unit = x.unit;
@@ -554,7 +579,7 @@ __device__ __forceinline__ void open_set(const AttnArgs& a, Fetch* f, int item, 
 }
 // The next run: of the unit, or of the next one with steps before place `end`.  Not inlined:
 // a copy in each loop costs more in instruction cache misses than the call.
-__device__ __noinline__ void open_run(const AttnArgs& a, Fetch* f, int end) {
+__device__ __noinline__ void open_run(const Call& a, Fetch* f, int end) {
     while (f->left == 0) {
         int item = f->item + f->pitch;
         if (f->u + 1 < f->nu) {
@@ -564,7 +589,7 @@ __device__ __noinline__ void open_run(const AttnArgs& a, Fetch* f, int end) {
         } else {
             Set x;  // the next set starts no later than a unit would
             item = f->item + 1;
-            const int u = item < end ? find(a, a.group, item, x) : 0;
+            const int u = item < end ? find(a, item, x) : 0;
             if (item >= end) break;
             open_set(a, f, item, x, u);
         }
@@ -575,13 +600,12 @@ __device__ __noinline__ void open_run(const AttnArgs& a, Fetch* f, int end) {
 
 constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + (int)sizeof(Fetch) + 127) / 128 * 128;  // ring, its barriers, Fetch
 
-__global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ Call a) {
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_kv = a.rows.n_kv, G = a.group;
     // a full grid: the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
     // neighbouring shares, so that their sum differs by at most one unit between schedulers
-    const int work = a.item_start[a.rows.n_streams];
+    const int work = a.end;
     const int per = a.per_sm, sms = gridDim.x / per;
     const long share = ((long)(blockIdx.x % sms) * kWarps + warp) * per + blockIdx.x / sms, shares = (long)gridDim.x * kWarps;
     int i = (int)(share * work / shares);
@@ -590,15 +614,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     pdl_trigger();
     if (i >= end) return;
     Set x;
-    int u = find(a, G, i, x);
+    int u = find(a, i, x);
     if (i >= end) return;  // no unit starts in the share
 
     char* buf = smem + warp * kWarpBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
     Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
-    const int page0 = __ldg(a.rows.kv[x.s].table + min(u * x.unit * kStepKeys, x.last) / kPage);
+    const int page0 = __ldg(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
     RawQuery raw;
-    ask_query(raw, a, x, G);  // before the keys, which they would wait behind
+    ask_query(raw, a, x);  // before the keys, which they would wait behind
     int fslot = 0;
     auto fetch = [&]() {
         if (lane == 0) {
@@ -607,7 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             if (run == 0) {
                 run = f->next_run;
                 if (run > 0) {
-                    src = f->heads + (size_t)asked_word(&f->page) * n_kv * kTileBytes + f->k % kPage / kBlockPos * kBlockBytes;
+                    src = f->heads + asked_word(&f->page) * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
                     f->k += run * kStepKeys;
                     f->left -= run;
                     open_run(a, f, end);
@@ -630,7 +654,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
         if (f->left > 0) {  // the first run, at once
             const int run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
             asked = min(run, kStages);
-            const char* src = f->heads + (size_t)page0 * n_kv * kTileBytes + f->k % kPage / kBlockPos * kBlockBytes;
+            const char* src = f->heads + page0 * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
             for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
             f->next = src;
             f->run = run - asked;
@@ -677,7 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             steps(Bool<false>());
         finish(e);
         if (a.direct) {
-            const OutRows o = out_rows(a, x, G);
+            const OutRows o = out_rows(a, x);
             const float R[2] = {1.f / e.l[0], 1.f / e.l[1]};
 #pragma unroll
             for (int d = 0; d < 8; ++d) put_out(o, d, f4(e.o[d]), R);
@@ -698,9 +722,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
         } else {
             if (++i >= end) break;
             fresh = true;
-            u = find(a, G, i, x);
+            u = find(a, i, x);
             if (i >= end) break;
-            ask_query(raw, a, x, G);
+            ask_query(raw, a, x);
         }
     }
     if (!there) {  // the copies in flight end before the CTA does, or these waits run out too
@@ -759,17 +783,15 @@ __device__ __forceinline__ void join(const float* pm, const float* pl, const flo
 // One tile (of a set's eight) per CTA: its warps join groups of kFan units, warp 0 the
 // groups.  A group's loads are all in flight at once, so the kernel costs about two
 // round trips to the L2, however many units.
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Call a) {
     extern __shared__ __align__(16) float4 js[];  // [group]: 32 x float4 output, then 8 + 8 maxima and sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-    const int G = a.group;
-    // the tile's set: the item of its unit 0
     const int d = blockIdx.x % 8, set = blockIdx.x / 8;
-    int s = 0;
-    while (s + 1 < a.rows.n_streams && set >= a.set_start[s + 1] * a.rows.n_kv) ++s;
+    int p = 0;
+    while (p + 1 < a.n_parts && set >= a.part[p + 1].set0 * a.n_kv) ++p;
     Set x;
-    int at0 = a.item_start[s] + (set - a.set_start[s] * a.rows.n_kv) * a.pitch_set[s];
-    find(a, G, at0, x);
+    int at0 = a.start[p] + (set - a.part[p].set0 * a.n_kv) * a.part[p].pitch_set;
+    find(a, at0, x);
     const int groups = (x.nu + kFan - 1) / kFan;
     constexpr int kGroup4 = 36;  // float4 of a group
     pdl_wait();
@@ -819,7 +841,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         return;
     }
     const float inv[2] = {1.f / L[0], 1.f / L[1]};
-    put_out(out_rows(a, x, G), d, O, inv);
+    put_out(out_rows(a, x), d, O, inv);
 }
 
 cudaLaunchConfig_t cfg(int grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
@@ -855,65 +877,81 @@ cudaError_t init_attn() {
     return e;
 }
 
-cudaError_t launch_attn(AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
-    if (a.rows.n_rows < 1) return cudaSuccess;
-    // a stream whose rows lie on both sides of a change of the unit's size (always a multiple of 32) becomes two
-    Rows& m = a.rows;
+cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
+    const Rows& m = a.rows;
+    if (m.n_rows < 1) return cudaSuccess;
+    const int G = a.n_q / m.n_kv;
+    Call c;
+    c.n_kv = m.n_kv;
+    c.group = G;
+    c.group_inv = (65536 + G - 1) / G;
+    c.max_units = a.max_units;
+    c.q = a.q;
+    c.ldq = a.ldq;
+    c.out = a.out;
+    c.ldo = a.ldo;
+    c.pm = a.pm;
+    c.pl = a.pl;
+    c.po = a.po;
+    c.status = a.status;
+    // A stream whose rows lie on both sides of a change of the unit's length (always at a multiple of 32) is
+    // two parts.  The work in places where a unit is its steps and one more (its start and end), a set's last
+    // unit as long as it is and two more (the set's queries):
+    int n = 0, most = 1, sets = 0, units = 0, places = 0, top_unit = 0, low_unit = 1 << 20;
+    int steps[kMaxParts];
     for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s], last = m.pos0[s] + R - 1;
-        a.unit[s] = unit_steps(m.pos0[s], m.n_kv);
-        if (R < 2 || unit_steps(last, m.n_kv) == a.unit[s]) continue;
-        for (int t = m.n_streams; t > s; --t) {
-            m.row_start[t + 1] = m.row_start[t];
-            m.pos0[t] = m.pos0[t - 1];
-            m.kv[t] = m.kv[t - 1];
+        int rows = m.row_start[s + 1] - m.row_start[s], row = m.row_start[s], pos = m.pos0[s];
+        while (rows > 0) {
+            Part& p = c.part[n];
+            p.unit = unit_steps(pos, m.n_kv);
+            p.rows = unit_steps(pos + rows - 1, m.n_kv) == p.unit ? rows : (pos + rows - 1) / kStepKeys * kStepKeys - pos;
+            p.row0 = row;
+            p.pos0 = pos;
+            p.heads = m.kv[s].pages + (size_t)m.layer * m.kv[s].n_pages * m.n_kv * kTileBytes;
+            p.table = m.kv[s].table;
+            p.page_bytes = (size_t)m.n_kv * kTileBytes;
+            p.set0 = sets;
+            steps[n] = (pos + p.rows - 1) / kStepKeys + 1;
+            p.nu = (steps[n] + p.unit - 1) / p.unit;
+            const int chunks = (p.rows * G + 7) / 8;
+            sets += chunks;
+            units += chunks * m.n_kv * p.nu;
+            places += chunks * m.n_kv * (steps[n] + p.nu + 2);
+            most = std::max(most, p.nu);
+            top_unit = std::max(top_unit, p.unit);
+            low_unit = std::min(low_unit, p.unit);
+            rows -= p.rows;
+            row += p.rows;
+            pos += p.rows;
+            ++n;
         }
-        m.pos0[s + 1] = last / kStepKeys * kStepKeys;
-        m.row_start[s + 1] = m.row_start[s] + m.pos0[s + 1] - m.pos0[s];
-        ++m.n_streams;
     }
-    const int G = a.group = a.n_q / m.n_kv;
-    a.group_inv = (65536 + G - 1) / G;
-    auto steps_of = [&](int s) { return (m.pos0[s] + m.row_start[s + 1] - m.row_start[s] - 1) / kStepKeys + 1; };
-    int most = 1, sets = 0, units = 0, steps = 0, top_unit = 0, low_unit = 1 << 20;
-    for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s], nu = (steps_of(s) + a.unit[s] - 1) / a.unit[s];
-        a.set_start[s] = sets;
-        if (R == 0) continue;
-        const int chunks = (R * G + 7) / 8;
-        sets += chunks;
-        units += chunks * m.n_kv * nu;
-        steps += chunks * m.n_kv * (steps_of(s) + nu + 2);
-        top_unit = std::max(top_unit, a.unit[s]);
-        low_unit = std::min(low_unit, a.unit[s]);
-        if (nu > most) most = nu;
-    }
-    // As many warps as there are units, one each, or a full grid whose warps share the work.  On the
-    // scale it is shared out by, a unit is its steps and one more (its start and end), a set's last
-    // unit as long as it is and two more (the set's queries); or, if all units have the same steps
-    // and that leaves the warp with the most work less, a unit is one.  SHARETEXT
+    c.n_parts = n;
+    // As many warps as there are units, one each, or a full grid whose warps share the places; or the units,
+    // if all have the same steps and that leaves the warp with the most work less.  SHARETEXT
     const int full = sms * kCtas, need = (units + kWarps - 1) / kWarps, warps = full * kWarps;
-    a.per_sm = need < full ? 1 : kCtas;
+    c.per_sm = need < full ? 1 : kCtas;
     bool count = need <= full;
-    if (!count && top_unit == low_unit) count = (units + warps - 1) / warps * (top_unit + 1) < (steps + warps - 1) / warps + top_unit;
-    int work = 0;  // below 2^29: at most 160 sets of columns, 64 heads, 2^15 steps and as many units
-    for (int s = 0; s < m.n_streams; ++s) {
-        const int R = m.row_start[s + 1] - m.row_start[s], nu = (steps_of(s) + a.unit[s] - 1) / a.unit[s];
-        a.pitch[s] = count ? 1 : a.unit[s] + 1;
-        a.pitch_set[s] = count ? nu : steps_of(s) + nu + 2;
-        a.item_start[s] = work;
-        if (R > 0) work += (R * G + 7) / 8 * m.n_kv * a.pitch_set[s];
+    if (!count && top_unit == low_unit)
+        count = (units + warps - 1) / warps * (top_unit + 1) < (places + warps - 1) / warps + top_unit;
+    int at = 0;  // below 2^29: at most 160 sets of columns, 64 heads, 2^15 steps and as many units
+    for (int i = 0; i < n; ++i) {
+        Part& p = c.part[i];
+        p.pitch = count ? 1 : p.unit + 1;
+        p.pitch_set = count ? p.nu : steps[i] + p.nu + 2;
+        c.start[i] = at;
+        at += (p.rows * G + 7) / 8 * m.n_kv * p.pitch_set;
     }
-    a.item_start[m.n_streams] = work;
-    a.direct = most == 1;
+    c.end = at;
+    c.direct = most == 1;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t c = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);
-    const cudaError_t e = cudaLaunchKernelEx(&c, units_kernel, a);
-    if (e != cudaSuccess || a.direct) return e;
+    cudaLaunchConfig_t g = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);
+    const cudaError_t e = cudaLaunchKernelEx(&g, units_kernel, c);
+    if (e != cudaSuccess || c.direct) return e;
     const int groups = (most + kFan - 1) / kFan;
-    c = cfg(sets * m.n_kv * 8, std::min(groups, sets * m.n_kv * 8 > sms ? kManyJoinWarps : kJoinWarps) * 32, groups > 1 ? groups * kGroupBytes : 0,
-            st, attr, true);
-    return cudaLaunchKernelEx(&c, join_kernel, a);
+    g = cfg(sets * m.n_kv * 8, std::min(groups, sets * m.n_kv * 8 > sms ? kManyJoinWarps : kJoinWarps) * 32,
+            groups > 1 ? groups * kGroupBytes : 0, st, attr, true);
+    return cudaLaunchKernelEx(&g, join_kernel, c);
 }
 
 }  // namespace kv4
