@@ -23,13 +23,23 @@
 // of the largest.  Likewise m moves only when an x_t passes it by 8.  Both decisions
 // are a column's own, so a column's bits do not depend on its neighbours.
 //
-// Split.  A unit is 128 or 256 keys of a KV head and up to eight columns at absolute positions, taken by one warp in
-// steps of 32 with a fresh (m, l, c, output).  A second kernel joins the units: groups
-// of 16, then the groups, in order.  So the bits depend on the position alone, however
-// the units are spread: the grid is persistent, each warp takes an equal share of the
-// call's units one after the other, and meets no other warp.  A warp's keys come by
-// bulk copies that one of its lanes asks for, into shared memory that no other warp
-// reads, always kStages - 1 steps ahead.
+// Split.  A unit is some steps of 32 keys of a KV head for up to eight columns, taken by
+// one warp with a fresh (m, l, c, output).  A second kernel joins the units: groups of 8,
+// then the groups, in order.  A unit's length comes from the row's position and the
+// cache's heads, so a row's bits do not depend on what else the call holds or how its
+// units are spread: the grid is persistent, each warp takes an equal share of the call's
+// work one unit after the other, and meets no other warp.  A warp's keys come by bulk
+// copies that one of its lanes asks for, into shared memory that no other warp reads.
+//
+// What bounds it.  One row over a long cache: after some 4 us (launch, parameters,
+// queries, the table, the first keys) the warps take a step in 1.15 us each, 7.3 TB/s
+// over all of them, until the cache is read; the join adds 5 us.  131,072 positions of 8
+// KV heads, seven query heads each (151 MB): 35 us, 4.3 TB/s on the whole.  Windows and
+// batches of short caches: the half-rate pipes that take codes apart and make operands
+// of them (some 700 cycles of a scheduler per 32 keys and eight columns, of which the
+// tensor pipe has 380), a unit's start and end (1.2 us of a warp: its code comes from
+// beyond the first instruction cache) and the partials, 4 KB per unit and eight columns,
+// which the join reads back: 16 rows over 4,096 keys 24.5 us, 16 rows over 8,192 each 32 us.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -45,16 +55,28 @@ namespace {
 constexpr int kStepKeys = 32;                      // two blocks of the cache
 constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
 // Steps of a unit, by the position of the row that attends and the cache's heads:
-// UNITTEXT
+// as long as that leaves every warp of a full grid at most one unit, but not below a
+// shortest: more steps mean fewer starts and partials, fewer mean more warps for one short
+// cache.  8 KV heads, seven query heads each.  Shortest before position 8,192, with 8 | 4 | 2
+// steps: one row over 4,096 keys 12.4 | 8.9 | 7.7 us, 16 rows over up to 8,192 each 34.1 |
+// 34.3 | 45.6 us.  From there on, with 4 | 5 | 6 | 8: rows over 1 to 32,000 keys 60.5 | 58.5
+// | 59.1 | 49.5 us.  One row over 131,072 keys with 8 steps, two or three units to a warp: 43
+// us, with 18 and one unit: 34 us.
 constexpr int kSpread = 152 * 12;                  // warps of the full grid
 __host__ inline int unit_steps(int pos, int n_kv) {
     const int most = kSpread / n_kv, steps = pos / kStepKeys + 1;
     return std::max(pos < 8192 ? 4 : 8, (steps + most - 1) / most);
 }
 constexpr int kWarps = 4;                          // of a CTA
-constexpr int kCtas = 3, kStages = 3;              // CTAs of an SM, steps of a warp's ring
-constexpr int kFan = 8;                            // units joined at a time
-constexpr int kJoinWarps = 16, kManyJoinWarps = 4;  // of a CTA: on a grid of at most a CTA per SM, or more
+// CTAs of an SM and steps of a warp's ring.  168 registers a thread allow three CTAs (four, at
+// 128, spill).  16 rows over up to 8,192 keys each with rings of 2 | 3 | 4: 31.6 | 33.1 | 35.8 us,
+// with two CTAs and rings of 4 | 6: 37.4 | 39.9 us.
+constexpr int kCtas = 3, kStages = 2;
+constexpr int kFan = 8;                           // units joined at a time
+// Warps of a CTA of the join, on a grid of at most a CTA per SM, or more.  16 rows over up to
+// 8,192 keys with 4 | 16: 32.9 | 35.3 us (groups of 16 units, 2 | 16 warps: 32.6 | 34.2 us; a
+// window of 16 rows over 4,096 keys prefers 8: 24.5 against 25.3 us).
+constexpr int kJoinWarps = 16, kManyJoinWarps = 4;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
 constexpr int kMaxJoinBytes = (kSpread + kFan - 1) / kFan * kGroupBytes;
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
@@ -928,7 +950,9 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     }
     c.n_parts = n;
     // As many warps as there are units, one each, or a full grid whose warps share the places; or the units,
-    // if all have the same steps and that leaves the warp with the most work less.  SHARETEXT
+    // if all have the same steps and that leaves the warp with the most work less.  By
+    // units | by places: 16 rows over up to 8,192 keys 35.0 | 38.2 us, 16 rows of one stream over 4,096 keys
+    // 26.8 | 25.9 us.
     const int full = sms * kCtas, need = (units + kWarps - 1) / kWarps, warps = full * kWarps;
     c.per_sm = need < full ? 1 : kCtas;
     bool count = need <= full;
