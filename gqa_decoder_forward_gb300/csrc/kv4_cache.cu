@@ -15,7 +15,7 @@ namespace kv4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = kThreads / 16;  // (row, head) items of a CTA
+constexpr int kRows = kThreads / 16;   // of a CTA of the write, of one head's keys or values
 constexpr float kRound = 12582912.f;   // 1.5 * 2^23, in bits 0x4b400000
 constexpr uint32_t kRoundCodes = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8);  // (<< 12 and more: 0)
 
@@ -83,14 +83,11 @@ __device__ __forceinline__ void write8(const bf16* x8, const uint4& raw, char* h
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
     pdl_wait();
     pdl_trigger();
-    const unsigned n_kv = a.rows.n_kv, n_items = (unsigned)a.rows.n_rows * n_kv;  // at most 2^30
-    const unsigned item = blockIdx.x * kItems + threadIdx.x / 16, it = min(item, n_items - 1);
-    const int lane = threadIdx.x & 15;
-    const bool live = item < n_items;  // whole half-warps; the others take part in the shuffles
-    const int r = (int)(it / n_kv), h = (int)(it - r * n_kv);
+    const int row = blockIdx.x * kRows + threadIdx.x / 16, lane = threadIdx.x & 15;
+    const bool live = row < a.rows.n_rows;  // whole half-warps; the others take part in the shuffles
+    const int r = min(row, a.rows.n_rows - 1), h = blockIdx.y >> 1, kind = blockIdx.y & 1;
     const int s = stream_of(a.rows, r);
     const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
-    const int kind = blockIdx.y;
     const long src = (a.wrap ? 2l * kPage * s + pos % kPage : r) * a.ld + (long)h * kHeadDim + lane * 8;
     const bf16* x8 = (kind ? a.v : a.k) + src;
     const uint4 raw = *reinterpret_cast<const uint4*>(x8);
@@ -167,9 +164,8 @@ cudaLaunchConfig_t cfg(long blocks, cudaStream_t st, cudaLaunchAttribute* attr, 
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st, bool pdl) {
     if (a.rows.n_rows < 1) return cudaSuccess;
     cudaLaunchAttribute attr[1];
-    const long items = (long)a.rows.n_rows * a.rows.n_kv;
-    cudaLaunchConfig_t c = cfg((items + kItems - 1) / kItems, st, attr, pdl);
-    c.gridDim.y = 2;
+    cudaLaunchConfig_t c = cfg((a.rows.n_rows + kRows - 1) / kRows, st, attr, pdl);
+    c.gridDim.y = 2 * a.rows.n_kv;
     return cudaLaunchKernelEx(&c, write_kernel, a);
 }
 
