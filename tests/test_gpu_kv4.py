@@ -432,7 +432,7 @@ def test_calls_that_are_refused_change_nothing():
 
 @pytest.mark.parametrize("pos0", [8186, 16378, 511 - 6])
 def test_windows_across_a_group_of_units_equal_single_rows_call_after_call(pos0):
-    """512 keys a unit, 16 units a group: rows on both sides of the border, several calls of one object."""
+    """Rows on both sides of a change of the units' length, number and groups, several calls of one object."""
     rows = 12
     kv, kq, vq = filled(140, 2, pos0 + rows, pos0 + rows)
     q = queries(141, rows, 14)
@@ -481,18 +481,17 @@ def values64(x):
 
 
 def test_many_units_on_single_warps_equal_few_units_on_whole_ctas():
-    """A call of many (unit, KV head) pairs gives each unit to a warp, one of few gives each element of a unit to a warp, and
-    wide windows take two tiles of columns: the same bits."""
+    """Calls of few and of many (unit, KV head) pairs, of one tile of columns and of two: the same bits."""
     n_kv, pos0, rows = 64, 8300, 9
     kv, kq, vq = filled(160, n_kv, pos0 + rows, pos0 + rows)
     q = queries(161, rows, n_kv)
     attn = tfl.KV4Attention(n_kv, n_kv, max_rows=16, max_positions=pos0 + rows)
     window = attend(attn, [kv], [pos0], [rows], q)                     # two tiles
-    one = attend(attn, [kv], [pos0], [8], q[:8])                       # one tile, 17 units x 64 heads
+    one = attend(attn, [kv], [pos0], [8], q[:8])                       # one tile x 64 heads
     several = attend(attn, [kv] * 9, [pos0 + i for i in range(9)], [1] * 9, q)
     assert (one == window[:8]).all() and (several == window).all()
     check(window[:1], q[:1], [pos0], kq, vq)
-    kv8, _, _ = filled(162, 8, 70000, 70000)                           # 137 units x 8 heads
+    kv8, _, _ = filled(162, 8, 70000, 70000)                           # units of 10 steps, which begin anywhere in a page
     q8 = queries(163, 2, 56)
     few = tfl.KV4Attention(56, 8, max_rows=16, max_positions=70000)
     for p in (69999, 66047, 66048, 65600):
@@ -524,3 +523,39 @@ def test_codes_next_to_halves_and_of_every_scale():
         np.testing.assert_array_equal(s, scale)
         np.testing.assert_array_equal(z, zero)
         np.testing.assert_array_equal(a, code)
+
+
+@pytest.mark.parametrize("pos0", [3584 - 7, 4480 - 7, 8192 - 3])
+def test_windows_across_a_change_of_the_units_length(pos0):
+    """64 heads: units of 4, 5, 6 steps before and after 3,584 and 4,480, of 10 around 8,192; a permuted table."""
+    n_kv, rows = 64, 16
+    table = np.random.default_rng(1).permutation((pos0 + rows + 127) // 128).astype(np.int32)
+    kv, kq, vq = filled(180, n_kv, pos0 + rows, pos0 + rows, table=table)
+    q = queries(181, rows, n_kv)
+    attn = tfl.KV4Attention(n_kv, n_kv, max_rows=32, max_positions=pos0 + rows)
+    window = attend(attn, [kv], [pos0], [rows], q)
+    for i in (0, 2, 3, 6, 7, 15):
+        assert (attend(attn, [kv], [pos0 + i], [1], q[i: i + 1])[0] == window[i]).all()
+    twice = attend(attn, [kv, kv], [pos0, pos0], [rows, rows], np.concatenate([q, q]))  # each cut in two
+    assert (twice[:rows] == window).all() and (twice[rows:] == window).all()
+    check(window[[0, 15]], q[[0, 15]], [pos0, pos0 + 15], kq, vq)
+
+
+@pytest.mark.parametrize("pos0,rows", [
+    ([0, 31, 3583, 8185, 20000], [1, 7, 2, 16, 5]),    # units of two lengths: shared by steps
+    ([8190, 7000, 8190, 7001, 8000, 7777, 8190, 8191, 6000, 8190, 7999, 8190, 7400, 8190, 8100, 8190], [1] * 16),
+    ([4096, 0, 4090], [16, 1, 1]),                     # one length, shared by units or by steps
+    ([20000, 4, 20000], [16, 0, 16]),                  # more units than warps over one cache
+])
+def test_batches_on_a_full_grid_equal_each_stream_alone(pos0, rows):
+    n = max(p + r for p, r in zip(pos0, rows))
+    kv, kq, vq = filled(190, 8, n, n)
+    q = queries(191, sum(rows), 56)
+    attn = tfl.KV4Attention(56, 8, max_rows=64, max_positions=n)
+    got = attend(attn, [kv] * len(pos0), pos0, rows, q)
+    at = 0
+    for p, r in zip(pos0, rows):
+        if r:
+            assert (attend(attn, [kv], [p], [r], q[at: at + r]) == got[at: at + r]).all()
+            check(got[at: at + 1], q[at: at + 1], [p], kq, vq)
+        at += r
