@@ -781,6 +781,10 @@ int decode_kv4(tfl_model* m, tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_stre
     if (attn->n_q != c.n_q || attn->n_kv != c.n_kv)
         return fail(TFL_E_ARG, "an attention object for %d query / %d KV heads; the model has %d / %d", attn->n_q,
                     attn->n_kv, c.n_q, c.n_kv);
+    int dev = -1;
+    CK(cudaGetDevice(&dev));
+    if (attn->device != dev)
+        return fail(TFL_E_ARG, "the attention object is on device %d and the current device is %d", attn->device, dev);
     if (!workspace || ((uintptr_t)workspace & 255u)) return fail(TFL_E_ARG, "workspace NULL or not 256-byte aligned");
     const size_t need = tfl_kv4_step_workspace_bytes(m);
     if (ws_bytes < need) return fail(TFL_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);

@@ -65,10 +65,12 @@ __device__ __forceinline__ int stream_of(const Rows& m, int r) {
     return s;
 }
 
-// The tile of (layer, page of pos, head).
-__device__ __forceinline__ char* tile(const View& v, int layer, int n_kv, int pos, int head) {
-    const int page = __ldg(v.table + pos / kPage);
-    return v.pages + (((size_t)layer * v.n_pages + page) * n_kv + head) * (size_t)kTileBytes;
+// The physical page of pos: below v.n_pages in a sound table.
+__device__ __forceinline__ unsigned page_of(const View& v, int pos) { return (unsigned)__ldg(v.table + pos / kPage); }
+
+// The tile of (layer, page, head); of an entry outside the cache, one of the last page's.
+__device__ __forceinline__ char* tile(const View& v, int layer, int n_kv, unsigned page, int head) {
+    return v.pages + (((size_t)layer * v.n_pages + min(page, v.n_pages - 1u)) * n_kv + head) * (size_t)kTileBytes;
 }
 
 // The half block (kind 0: keys, 1: values) of a tile that holds pos.

@@ -312,6 +312,7 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
             return fail(TFL_E_CAPACITY, "stream %d: positions to %d pass the object's max_positions %d", s,
                         pos0[s] + rows[s] - 1, attn->max_pos);
     if (bad_ptr(q) || bad_ptr(out)) return fail(TFL_E_ARG, "q/out NULL or not 16-byte aligned");
+    if (q == out) return fail(TFL_E_ARG, "q and out are the same memory");
     if (bad_ld(ldq, attn->n_q) || bad_ld(ldo, attn->n_q))
         return fail(TFL_E_ARG, "ldq %zu / ldo %zu: less than %d heads of %d or not a multiple of 8", ldq, ldo,
                     attn->n_q, kHeadDim);

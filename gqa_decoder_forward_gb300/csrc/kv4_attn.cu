@@ -411,6 +411,7 @@ struct Part {
     const char* heads;             // tile 0 of the layer
     const int* table;
     size_t page_bytes;             // of the layer: n_kv tiles
+    unsigned last_page;            // what an entry of the table outside the cache is taken for
     int row0, pos0, rows;
     int unit, nu;                  // steps of a unit, units of a set
     int pitch, pitch_set, set0;    // set0: sets of columns before the part
@@ -571,13 +572,14 @@ struct Fetch {
     const char* heads;      // tile 0 of its layer and head
     const int* table;
     size_t page_bytes;
+    unsigned last_page;
 };
 __device__ __forceinline__ void ask_word(int* dst, const int* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ int asked_word(const int* dst) {
+__device__ __forceinline__ unsigned asked_word(const int* dst) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    return *reinterpret_cast<const volatile int*>(dst);
+    return *reinterpret_cast<const volatile unsigned*>(dst);
 }
 
 __device__ __forceinline__ void open_unit(Fetch* f, int v) {
@@ -592,6 +594,7 @@ __device__ __forceinline__ void open_set(const Call& a, Fetch* f, int item, cons
     f->heads = p.heads + x.h * kTileBytes;
     f->table = p.table;
     f->page_bytes = p.page_bytes;
+    f->last_page = p.last_page;
     f->item = item;
     f->nu = x.nu;
     f->unit = x.unit;
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     char* buf = smem + warp * kWarpBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
     Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
-    const int page0 = __ldg(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
+    const unsigned page0 = __ldg(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
     RawQuery raw;
     ask_query(raw, a, x);  // before the keys, which they would wait behind
     int fslot = 0;
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             if (run == 0) {
                 run = f->next_run;
                 if (run > 0) {
-                    src = f->heads + asked_word(&f->page) * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
+                    src = f->heads + min(asked_word(&f->page), f->last_page) * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
                     f->k += run * kStepKeys;
                     f->left -= run;
                     open_run(a, f, end);
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
         if (f->left > 0) {  // the first run, at once
             const int run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
             asked = min(run, kStages);
-            const char* src = f->heads + page0 * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
+            const char* src = f->heads + min(page0, f->last_page) * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
             for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
             f->next = src;
             f->run = run - asked;
@@ -932,6 +935,7 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
             p.heads = m.kv[s].pages + (size_t)m.layer * m.kv[s].n_pages * m.n_kv * kTileBytes;
             p.table = m.kv[s].table;
             p.page_bytes = (size_t)m.n_kv * kTileBytes;
+            p.last_page = m.kv[s].n_pages - 1;
             p.set0 = sets;
             steps[n] = (pos + p.rows - 1) / kStepKeys + 1;
             p.nu = (steps[n] + p.unit - 1) / p.unit;

@@ -91,7 +91,9 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     const long src = (a.wrap ? 2l * kPage * s + pos % kPage : r) * a.ld + (long)h * kHeadDim + lane * 8;
     const bf16* x8 = (kind ? a.v : a.k) + src;
     const uint4 raw = *reinterpret_cast<const uint4*>(x8);
-    write8(x8, raw, half_block(tile(a.rows.kv[s], a.rows.layer, a.rows.n_kv, pos, h), pos, kind), pos, live);
+    const View& kv = a.rows.kv[s];
+    const unsigned page = page_of(kv, pos);
+    write8(x8, raw, half_block(tile(kv, a.rows.layer, a.rows.n_kv, page, h), pos, kind), pos, live && page < (unsigned)kv.n_pages);
 }
 
 // Two bf16 numbers, each z + s n rounded once to fp32 and then to bf16.
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const int h = (int)((unsigned)item % (unsigned)n_kv), b = (int)((unsigned)item / (unsigned)n_kv);
     const int r0 = a.rows.row_start[s], pos0 = a.rows.pos0[s], end = pos0 + a.rows.row_start[s + 1] - r0;
     const int p0 = pos0 / kBlockPos * kBlockPos + b * kBlockPos;  // the block's first position
-    const char* hb = half_block(tile(a.rows.kv[s], a.rows.layer, n_kv, p0, h), p0, kind);
+    const char* hb = half_block(tile(a.rows.kv[s], a.rows.layer, n_kv, page_of(a.rows.kv[s], p0), h), p0, kind);
     uint32_t code[8], meta[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // rows i * 2 + half: what was never written is read but not used

@@ -473,7 +473,7 @@ int tfl_attention_decode_noalloc(tfl_kv* kv, int layer, int pos0, int rows, cons
  *   zero = min x,  scale = bf16((max x - min x) / 15),
  *   n = clamp(round((x - zero) / scale), 0, 15) (nearest, ties to even; 0 when scale = 0)
  * computed in fp32, and stands for zero + scale * n: at most half a scale from x,
- * plus the rounding of the scale (relative 2^-9, at most 15 * 2^-9 of a scale).
+ * plus the rounding of the scale (relative 2^-8, at most 15 * 2^-8 of a scale).
  * A group with a NaN or an infinity, or whose max - min overflows fp32, stands
  * for NaN in all its dims.
  *
@@ -486,7 +486,9 @@ int tfl_attention_decode_noalloc(tfl_kv* kv, int layer, int pos0, int rows, cons
  * the keys (bf16), then the same two parts for the values.  In a row, dims
  * 8c..8c+7 are the first and 64+8c..64+8c+7 the second 32-bit word of 8-byte chunk
  * c, the lowest dim in the lowest 4 bits; chunk c is stored as chunk c ^ 4 at
- * positions whose bit 1 is set.
+ * positions whose bit 1 is set.  Entries of the table are the caller's to permute
+ * between calls; one outside 0..n_pages-1 is not followed: rows there are not written,
+ * and what is read or attended in their place is some page of the cache.
  *
  * Independent of any model: layers 1..1024, n_kv 1..64 heads, head_dim 128, max_positions
  * 1..2^20.  bytes: 0 for sizes outside these.  tfl_kv4_alloc: dev_buf 16-byte

@@ -428,6 +428,36 @@ def test_calls_that_are_refused_change_nothing():
     same_bytes(host, kv)
 
 
+def test_queries_and_output_in_one_place_are_refused():
+    kv, _, _ = filled(175, 2, 40, 40)
+    q = torch.zeros((1, 8 * 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(tfl.TflError) as e:
+        tfl.tfl_kv4_attention(tfl.KV4Attention(8, 2, 1, 40), tfl.KV4Rows([kv], [39], [1]), 0, q, q)
+    assert e.value.code == tfl.TFL_E_ARG
+
+
+def test_table_entries_outside_the_cache_are_not_followed():
+    """Pages 1 and 3 of five outside: rows there are not written, rows that attend page 0 alone are as ever, reads and longer
+    rows end."""
+    n_kv, n = 2, 600
+    table = np.array([4, 5, 0, -7, 2], np.int32)
+    host, kv = make(1, n_kv, n, 0x11, table)
+    k, v = rows_like_keys(176, n, n_kv), rows_like_keys(177, n, n_kv)
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [n]), 0, cuda_bf16(k), cuda_bf16(v))
+    for a, b in ((0, 128), (256, 384), (512, 600)):
+        put_rows(host, 0, a, 0, k[a:b])
+        put_rows(host, 0, a, 1, v[a:b])
+    same_bytes(host, kv)
+    gk = torch.empty((n, n_kv, 128), dtype=torch.bfloat16, device="cuda")
+    gv = torch.empty_like(gk)
+    tfl.tfl_kv4_read(tfl.KV4Rows([kv], [0], [n]), 0, gk, gv)
+    torch.cuda.synchronize()
+    q = queries(178, 1, 8)
+    attn = tfl.KV4Attention(8, n_kv, max_rows=2, max_positions=n)
+    check(attend(attn, [kv], [127], [1], q), q, [127], ref.quantise(k), ref.quantise(v))
+    attend(attn, [kv], [n - 1], [1], q)
+
+
 # ---- long caches: partials joined in groups -------------------------------------------------
 
 @pytest.mark.parametrize("pos0", [8186, 16378, 511 - 6])
