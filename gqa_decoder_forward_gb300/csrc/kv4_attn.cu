@@ -743,6 +743,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             i += x.pitch;
             if (i >= end) break;
             fresh = false;
+            raw = RawQuery{};  // or its registers would be held through the unit
             ++u;
         } else {
             if (++i >= end) break;
