@@ -419,7 +419,8 @@ struct Part {
 struct Call {
     int n_parts, n_kv, group, group_inv;  // query heads per KV head; 65536 / group, rounded up
     int per_sm, direct, max_units;        // CTAs of an SM; every set has one unit, whose warp writes the output
-    int end;                              // places of the call
+    int end;                              // places of the call: share for each warp, share_rest over
+    unsigned share, share_rest;
     const bf16* q;
     long ldq;
     bf16* out;
@@ -628,23 +629,29 @@ constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + (int)sizeof(Fetch) + 12
 __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ Call a) {
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a full grid: the four warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
+    // a full grid: the warps that a scheduler of an SM gets (CTAs b, b + SMs, ...; the same warp of each) take
     // neighbouring shares, so that their sum differs by at most one unit between schedulers
-    const int work = a.end;
-    const int per = a.per_sm, sms = gridDim.x / per;
-    const long share = ((long)(blockIdx.x % sms) * kWarps + warp) * per + blockIdx.x / sms, shares = (long)gridDim.x * kWarps;
-    int i = (int)(share * work / shares);
-    const int end = (int)((share + 1) * work / shares);
-    pdl_wait();
-    pdl_trigger();
-    if (i >= end) return;
-    Set x;
-    int u = find(a, i, x);
-    if (i >= end) return;  // no unit starts in the share
-
+    const unsigned per = a.per_sm, sms = gridDim.x / per, shares = gridDim.x * kWarps;
+    const unsigned share = ((blockIdx.x % sms) * kWarps + warp) * per + blockIdx.x / sms;
+    // floor(share * end / shares), in 32 bits
+    int i = (int)(share * a.share + share * a.share_rest / shares);
+    const int end = (int)((share + 1) * a.share + (share + 1) * a.share_rest / shares);
     char* buf = smem + warp * kWarpBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + kStages * kStepBytes);
     Fetch* f = reinterpret_cast<Fetch*>(full + kStages);
+    Set x;
+    int u = 0;
+    if (i < end) u = find(a, i, x);
+    if (i < end && lane == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
+        mbar_init_fence();
+        f->run = 0;
+        open_set(a, f, i, x, u);
+    }
+    pdl_wait();  // memory from here on
+    pdl_trigger();
+    if (i >= end) return;  // no unit starts in the share
+
     const unsigned page0 = __ldg(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
     RawQuery raw;
     ask_query(raw, a, x);  // before the keys, which they would wait behind
@@ -672,10 +679,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     };
     int asked = 0;
     if (lane == 0) {
-        for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
-        mbar_init_fence();
-        f->run = 0;
-        open_set(a, f, i, x, u);
         if (f->left > 0) {  // the first run, at once
             const int run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
             asked = min(run, kStages);
@@ -974,6 +977,9 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
         at += (p.rows * G + 7) / 8 * m.n_kv * p.pitch_set;
     }
     c.end = at;
+    const unsigned shares = (need < full ? need : full) * kWarps;
+    c.share = at / shares;
+    c.share_rest = at % shares;
     c.direct = most == 1;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t g = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);

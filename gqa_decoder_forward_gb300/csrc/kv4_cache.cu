@@ -81,8 +81,6 @@ __device__ __forceinline__ void write8(const bf16* x8, const uint4& raw, char* h
 }
 
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
-    pdl_wait();
-    pdl_trigger();
     const int row = blockIdx.x * kRows + threadIdx.x / 16, lane = threadIdx.x & 15;
     const bool live = row < a.rows.n_rows;  // whole half-warps; the others take part in the shuffles
     const int r = min(row, a.rows.n_rows - 1), h = blockIdx.y >> 1, kind = blockIdx.y & 1;
@@ -90,6 +88,8 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     const int pos = a.rows.pos0[s] + (r - a.rows.row_start[s]);
     const long src = (a.wrap ? 2l * kPage * s + pos % kPage : r) * a.ld + (long)h * kHeadDim + lane * 8;
     const bf16* x8 = (kind ? a.v : a.k) + src;
+    pdl_wait();  // memory from here on
+    pdl_trigger();
     const uint4 raw = *reinterpret_cast<const uint4*>(x8);
     const View& kv = a.rows.kv[s];
     const unsigned page = page_of(kv, pos);
@@ -105,8 +105,6 @@ __device__ __forceinline__ uint32_t two(uint32_t code, int i, float s, float z) 
 
 // A warp per (block that a stream's rows touch, head, keys or values).
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 7, j = (lane >> 3) & 1;
     const int n_kv = a.rows.n_kv;
     int item = (int)((blockIdx.x * kThreads + threadIdx.x) / 32);
@@ -115,7 +113,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     int s = 0;
     while (s + 1 < a.rows.n_streams && item >= a.item_start[s + 1]) ++s;
     item -= a.item_start[s];
-    if (s == a.rows.n_streams - 1 && item >= a.item_start[s + 1] - a.item_start[s]) return;
+    const bool none = s == a.rows.n_streams - 1 && item >= a.item_start[s + 1] - a.item_start[s];
+    pdl_wait();  // memory from here on
+    pdl_trigger();
+    if (none) return;
     const int h = (int)((unsigned)item % (unsigned)n_kv), b = (int)((unsigned)item / (unsigned)n_kv);
     const int r0 = a.rows.row_start[s], pos0 = a.rows.pos0[s], end = pos0 + a.rows.row_start[s + 1] - r0;
     const int p0 = pos0 / kBlockPos * kBlockPos + b * kBlockPos;  // the block's first position
