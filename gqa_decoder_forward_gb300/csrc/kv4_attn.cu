@@ -34,12 +34,12 @@
 // What bounds it.  One row over a long cache: after some 4 us (launch, parameters,
 // queries, the table, the first keys) the warps take a step in 1.15 us each, 7.3 TB/s
 // over all of them, until the cache is read; the join adds 5 us.  131,072 positions of 8
-// KV heads, seven query heads each (151 MB): 35 us, 4.3 TB/s on the whole.  Windows and
+// KV heads, seven query heads each (151 MB): 34 us, 4.4 TB/s on the whole.  Windows and
 // batches of short caches: the half-rate pipes that take codes apart and make operands
 // of them (some 700 cycles of a scheduler per 32 keys and eight columns, of which the
 // tensor pipe has 380), a unit's start and end (1.2 us of a warp: its code comes from
 // beyond the first instruction cache) and the partials, 4 KB per unit and eight columns,
-// which the join reads back: 16 rows over 4,096 keys 24.5 us, 16 rows over 8,192 each 32 us.
+// which the join reads back: 16 rows over 4,096 keys 24 us, 16 rows over up to 8,192 each 31 us.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_fp16.h>
@@ -57,11 +57,12 @@ constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
 // Steps of a unit, by the position of the row that attends and the cache's heads:
 // as long as that leaves every warp of a full grid at most one unit, but not below a
 // shortest: more steps mean fewer starts and partials, fewer mean more warps for one short
-// cache.  8 KV heads, seven query heads each.  Shortest before position 8,192, with 8 | 4 | 2
-// steps: one row over 4,096 keys 12.4 | 8.9 | 7.7 us, 16 rows over up to 8,192 each 34.1 |
-// 34.3 | 45.6 us.  From there on, with 4 | 5 | 6 | 8: rows over 1 to 32,000 keys 60.5 | 58.5
-// | 59.1 | 49.5 us.  One row over 131,072 keys with 8 steps, two or three units to a warp: 43
-// us, with 18 and one unit: 34 us.
+// cache.  8 KV heads, seven query heads each.  Shortest before position 8,192, with 3 | 4 | 5 |
+// 6 | 8 steps: one row over 4,096 keys 7.9 | 8.1 | 9.0 | 9.7 | 11.2 us, 16 rows over up to
+// 8,192 each 33.6 | 31.1 | 33.4 | 29.7 | 33.4 us.  From there on, with 6 | 8 | 10 | 12: one row
+// over 9,000 keys 12.2 | 13.3 | 15.4 | 17.3 us, rows over 1 to 32,000 keys 47.6 | 45.2 | 42.8 |
+// 43.5 us, a window of 16 rows over 20,000 89 | 81 | 79 | 85 us.  One row over 131,072 keys with
+// 8 steps, two or three units to a warp: 43 us, with 18 and one unit: 34 us.
 constexpr int kSpread = 152 * 12;                  // warps of the full grid
 __host__ inline int unit_steps(int pos, int n_kv) {
     const int most = kSpread / n_kv, steps = pos / kStepKeys + 1;
