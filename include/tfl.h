@@ -537,7 +537,9 @@ int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
  * Rows past the last stream's are left as they were.  A cache may be named more
  * than once (several rows of a shared prompt).  A key or value that stands for NaN
  * makes the heads that attend it NaN; positions a row does not attend never
- * matter, whatever their bytes.
+ * matter, whatever their bytes.  Queries are to be below 2^115 in magnitude, values
+ * below 2^115 / (keys attended): beyond, fp16 operands or fp32 sums may overflow
+ * (to infinities or NaN).
  * A row's result depends on its own query and its cache alone, bit for bit: not
  * on the other rows, streams or the capacity.
  *

@@ -250,6 +250,19 @@ def test_sharp_and_flat_softmaxes_and_value_scales_that_differ():
     check(attend(attn, [kv], [n - 1], [1], q), q, [n - 1], ref.quantise(k), ref.quantise(v))
 
 
+@pytest.mark.parametrize("up,value", [(110, 104), (-110, -80), (0, 104), (60, -110)])
+def test_queries_and_values_far_from_one(up, value):
+    """Queries times 2^up with keys times 2^-up (the scores stay as they are), values times 2^value."""
+    n = 300
+    k, v = rows_like_keys(55, n, 2), rows_like_keys(56, n, 2)
+    k, v = k * np.float32(2.0 ** -up), v * np.float32(2.0 ** value)  # exact: bf16 numbers
+    _, kv = make(1, 2, n)
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [n]), 0, cuda_bf16(k), cuda_bf16(v))
+    q = queries(57, 1, 14) * np.float32(2.0 ** up)
+    attn = tfl.KV4Attention(14, 2, max_rows=1, max_positions=n)
+    check(attend(attn, [kv], [n - 1], [1], q), q, [n - 1], ref.quantise(k), ref.quantise(v))
+
+
 def test_streams_of_different_lengths_in_one_call():
     pos0, rows = [0, 15, 1023, 700, 130, 0, 511], [1, 7, 2, 0, 16, 3, 1]
     kvs, qs = [], []
