@@ -17,11 +17,12 @@
 //
 // The weights' operand is w = fp16(P s c), c a power of two per column: one rounding
 // of 2^-11 relative, far below the output's 2^-8, at half the tensor work of a split
-// into two numbers.  c starts so that the first 32 keys' largest w is 2^6..2^7 and
-// moves (with the running output) only when a w passes 2^15, so products down to
-// 2^-21 of the largest keep fp16's full 11 bits and smaller ones an absolute 2^-31
-// of the largest.  Likewise m moves only when an x_t passes it by 8.  Both decisions
-// are a column's own, so a column's bits do not depend on its neighbours.
+// into two numbers.  c is set, up or down, so that the largest w of 32 keys is 2^6..2^7:
+// at a unit's start, whenever m moves (which makes what came before smaller), and when a w
+// passes 2^15; the running output moves with it.  So products down to 2^-20 of the largest
+// keep fp16's full 11 bits and smaller ones an absolute 2^-31 of the largest.  m moves only
+// when an x_t passes it by 8.  Both decisions are a column's own, so a column's bits do not
+// depend on its neighbours.
 //
 // Split.  A unit is some steps of 32 keys of a KV head for up to eight columns, taken by
 // one warp with a fresh (m, l, c, output).  A second kernel joins the units: groups of 8,
@@ -281,13 +282,15 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
                                            (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
     }
     // A score passes m by more than 8, or a w passes 2^15: m, c and the running sums move in the
-    // columns where it does.  A unit's first step sets them.
+    // columns where it does.  A unit's first step sets them.  Where m moves, the keys before lose
+    // weight, and c, which they had set, is chosen anew.
     if (move) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float high = col_max(top[j]);
+            const bool up = high > e.m[j] + kLazy;
             float al = 1.f;
-            if (high > e.m[j] + kLazy) {
+            if (up) {
                 al = ex2(e.m[j] - high);
                 e.m[j] = high;
                 e.l[j] *= al;
@@ -308,9 +311,19 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
                     if (!EDGE || !hidden(j, b, hk)) ps = fmaxf(ps, x);
                 }
             ps = col_max(ps);
-            if (ps * e.c[j] > kTopW * pow2(-20) && ps < INFINITY) {
-                const float c = pow2(max(-100, min(100, 6 - 20 - exponent(ps))));
-                al *= c * inv_pow2(e.c[j]);  // powers of two: exact, or 0
+            // What the output holds, in units of ps: a bound on its largest product, at most 16 times the
+            // unit's keys too large.  (All lanes take part; only columns below use it.)
+            float kept = 0.f;
+            if (!first) {
+#pragma unroll
+                for (int d = 1; d < 8; d += 2) kept = fmaxf(kept, fmaxf(e.o[d][j], e.o[d][2 + j]));
+                kept = col_max(kept) * al * inv_pow2(e.c[j]);
+            }
+            if ((up || ps * e.c[j] > kTopW * pow2(-20)) && ps < INFINITY) {
+                // c follows what is kept only where that is 2^20 times the new products (it is held in
+                // fp32, and this bounds it too), so the largest product is at 2^6 or above.
+                const float c = pow2(max(-100, min(100, 6 - 20 - exponent(fmaxf(ps, kept * pow2(-20))))));
+                al = fminf(al * c * inv_pow2(e.c[j]), FLT_MAX);  // finite where the output is 0
                 e.c[j] = c;
             }
             if (!first) {

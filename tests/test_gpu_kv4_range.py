@@ -1,0 +1,37 @@
+"""Attention over the 4-bit cache where the scales of values, and the scores, lie far apart: the
+operand scales that the kernel keeps per column, against the 64-bit restatement and its bound."""
+import numpy as np
+import pytest
+
+from gqa_decoder_forward_gb300 import tfl
+from tests import kv4_ref as ref
+from tests.test_gpu_kv4 import _built, attend, check, cuda_bf16, make, queries, rows_like_keys  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(x):
+    return ref.from_bits(ref.bf16_bits(np.asarray(x, np.float32)))
+
+
+def cache_of(k, v):
+    """A library cache of rows k, v [n, n_kv, 128], what is never written reading as NaN."""
+    _, kv = make(1, k.shape[1], k.shape[0], 0xFF)
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [k.shape[0]]), 0, cuda_bf16(k), cuda_bf16(v))
+    return kv
+
+
+@pytest.mark.parametrize("n", [128, 700])
+@pytest.mark.parametrize("up", [24, 30, 40])
+def test_large_values_of_low_scores_before_ordinary_values_of_high_ones(n, up):
+    """The first 32 keys of every 128 have values 2^up times the others' and, in some columns, scores some 60
+    (log2) below theirs: they set a unit's operand scale and then weigh nothing."""
+    k, v = rows_like_keys(200, n, 1), rows_like_keys(201, n, 1)
+    first = np.arange(n) % 128 < 32
+    v[first] *= np.float32(2.0 ** up)
+    k[:, 0, 0] = np.where(first, -30.0, 0.0)
+    kv = cache_of(k, v)
+    q = queries(202, 1, 8)
+    q[0, :, 0] = [16, 17, -16, 0, 8, 4, 30, 2]   # 0.1275 x 30 x 16 = 61
+    attn = tfl.KV4Attention(8, 1, max_rows=1, max_positions=n)
+    check(attend(attn, [kv], [n - 1], [1], q), q, [n - 1], ref.quantise(k), ref.quantise(v))
