@@ -15,12 +15,12 @@
 // numbers 2^-26 and less of the largest); scales, zeros, weights, maxima and sums
 // are fp32.
 //
-// The weights' operand is w = fp16(P s c), c a power of two per column: one rounding
+// The weights' operand is w = fp16(P s c), c a power of two per column and group: one rounding
 // of 2^-11 relative, far below the output's 2^-8, at half the tensor work of a split
 // into two numbers.  c is set, up or down, so that the largest w of 32 keys is 2^6..2^7:
 // at a unit's start, whenever m moves (which makes what came before smaller), and when a w
-// passes 2^15; the running output moves with it.  So products down to 2^-20 of the largest
-// keep fp16's full 11 bits and smaller ones an absolute 2^-31 of the largest.  m moves only
+// passes 2^15; the running output moves with it.  So products P s down to 2^-20 of the group's
+// largest keep fp16's full 11 bits and smaller ones an absolute 2^-31 of it.  m moves only
 // when an x_t passes it by 8.  Both decisions are a column's own, so a column's bits do not
 // depend on its neighbours.
 //
@@ -148,6 +148,13 @@ __device__ __forceinline__ float col_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
+// Of two numbers, neither below 0: the upper halves of their bits.
+__device__ __forceinline__ uint32_t col_max2(float lo, float hi) {
+    uint32_t x = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
 __device__ __forceinline__ float col_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 4);
     x += __shfl_xor_sync(0xffffffffu, x, 8);
@@ -168,7 +175,7 @@ struct Query {
 };
 
 struct State {
-    float m[2], l[2], c[2], za[2][2];  // l and za: this lane's keys only
+    float m[2], l[2], c[2][2], za[2][2];  // [column], c and za [column][group]; l and za: this lane's keys only
     float o[8][4];  // sums over codes, in units of c and of the codes: tiles 2i the low codes, 2i + 1 whole bytes
 };
 
@@ -177,7 +184,7 @@ __device__ __forceinline__ void reset(State& e) {
     for (int j = 0; j < 2; ++j) {
         e.m[j] = kUnset;
         e.l[j] = 0.f;
-        e.c[j] = pow2(100);
+        e.c[j][0] = e.c[j][1] = pow2(100);
         e.za[j][0] = e.za[j][1] = 0.f;
     }
 #pragma unroll
@@ -249,9 +256,8 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
         float w[2][2];  // [group][column]
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float pc = p[b][hk][j] * e.c[j];
-            w[0][j] = pc * lo_f(vm.x);
-            w[1][j] = pc * lo_f(vm.y);
+            w[0][j] = p[b][hk][j] * e.c[j][0] * lo_f(vm.x);
+            w[1][j] = p[b][hk][j] * e.c[j][1] * lo_f(vm.y);
         }
         if (EDGE) {
 #pragma unroll
@@ -285,6 +291,15 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
     // columns where it does.  A unit's first step sets them.  Where m moves, the keys before lose
     // weight, and c, which they had set, is chosen anew.
     if (move) {
+        // What the output holds, by column: of both groups the upper halves of the largest number (0: nothing yet).
+        uint32_t held[2] = {0, 0};
+        float to[2][2];  // the output's factors [column][group]
+        if (!first) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                held[j] = col_max2(fmaxf(fmaxf(e.o[1][j], e.o[1][2 + j]), fmaxf(e.o[3][j], e.o[3][2 + j])),
+                                   fmaxf(fmaxf(e.o[5][j], e.o[5][2 + j]), fmaxf(e.o[7][j], e.o[7][2 + j])));
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float high = col_max(top[j]);
@@ -301,38 +316,40 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk) p[b][hk][j] = ex2(raw[b][hk][j] - e.m[j]);
-            float ps = 0.f;  // largest P s 2^-20 (which cannot overflow)
+            float ps[2] = {0.f, 0.f};  // largest P s 2^-20 (which cannot overflow), by group
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk) {
                     const uint2 vm = v_meta(b, hk);
-                    const float x = p[b][hk][j] * (fmaxf(lo_f(vm.x), lo_f(vm.y)) * pow2(-20));
-                    if (!EDGE || !hidden(j, b, hk)) ps = fmaxf(ps, x);
+                    const float pk = p[b][hk][j] * pow2(-20);
+                    if (!EDGE || !hidden(j, b, hk)) {
+                        ps[0] = fmaxf(ps[0], pk * lo_f(vm.x));
+                        ps[1] = fmaxf(ps[1], pk * lo_f(vm.y));
+                    }
                 }
-            ps = col_max(ps);
-            // What the output holds, in units of ps: a bound on its largest product, at most 16 times the
-            // unit's keys too large.  (All lanes take part; only columns below use it.)
-            float kept = 0.f;
-            if (!first) {
+            const uint32_t most = col_max2(ps[0], ps[1]);
 #pragma unroll
-                for (int d = 1; d < 8; d += 2) kept = fmaxf(kept, fmaxf(e.o[d][j], e.o[d][2 + j]));
-                kept = col_max(kept) * al * inv_pow2(e.c[j]);
-            }
-            if ((up || ps * e.c[j] > kTopW * pow2(-20)) && ps < INFINITY) {
-                // c follows what is kept only where that is 2^20 times the new products (it is held in
-                // fp32, and this bounds it too), so the largest product is at 2^6 or above.
-                const float c = pow2(max(-100, min(100, 6 - 20 - exponent(fmaxf(ps, kept * pow2(-20))))));
-                al = fminf(al * c * inv_pow2(e.c[j]), FLT_MAX);  // finite where the output is 0
-                e.c[j] = c;
-            }
-            if (!first) {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    e.o[d][j] *= al;
-                    e.o[d][2 + j] *= al;
+            for (int gr = 0; gr < 2; ++gr) {
+                const bool over = __ballot_sync(0xffffffffu, ps[gr] * e.c[j][gr] > kTopW * pow2(-20)) & (0x11111111u << t);
+                // In units of ps, what is held is a bound on its largest product, at most 16 times the unit's keys
+                // too large.  c follows it only where that is 2^20 times the new products (it is in fp32,
+                // and this bounds it too), so the largest product is at 2^6 or above.
+                const float kept = (gr ? hi_f(held[j]) : lo_f(held[j])) * al * inv_pow2(e.c[j][gr]);
+                const int x = max(exponent(gr ? hi_f(most) : lo_f(most)), exponent(kept) - 20);
+                to[j][gr] = al;
+                if ((up || over) && x < 128) {  // 128: an infinity, whose output is not finite anyway
+                    const float now = pow2(max(-100, min(100, 6 - 20 - x)));
+                    to[j][gr] = fminf(al * now * inv_pow2(e.c[j][gr]), FLT_MAX);  // finite where the output is 0
+                    e.c[j][gr] = now;
                 }
             }
+        }
+        if (!first) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e.o[d][k] *= to[k & 1][d >> 2];
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -400,11 +417,12 @@ __device__ __forceinline__ void finish(State& e) {
     for (int j = 0; j < 2; ++j) {
         e.l[j] = col_sum(e.l[j]);
         const float z[2] = {col_sum(e.za[j][0]), col_sum(e.za[j][1])};
-        const float inv = inv_pow2(e.c[j]), lo = inv * kLoCode, hi = inv * kHiCode;  // c >= 2^-100
+        const float inv[2] = {inv_pow2(e.c[j][0]), inv_pow2(e.c[j][1])};  // c >= 2^-100
 #pragma unroll
         for (int d = 0; d < 8; d += 2)
 #pragma unroll
             for (int k = j; k < 4; k += 2) {
+                const float lo = inv[d >> 2] * kLoCode, hi = inv[d >> 2] * kHiCode;
                 e.o[d + 1][k] = fmaf(e.o[d + 1][k] - e.o[d][k], hi, z[d >> 2]);
                 e.o[d][k] = fmaf(e.o[d][k], lo, z[d >> 2]);
             }

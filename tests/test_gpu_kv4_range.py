@@ -35,3 +35,21 @@ def test_large_values_of_low_scores_before_ordinary_values_of_high_ones(n, up):
     q[0, :, 0] = [16, 17, -16, 0, 8, 4, 30, 2]   # 0.1275 x 30 x 16 = 61
     attn = tfl.KV4Attention(8, 1, max_rows=1, max_positions=n)
     check(attend(attn, [kv], [n - 1], [1], q), q, [n - 1], ref.quantise(k), ref.quantise(v))
+
+
+@pytest.mark.parametrize("n", [40, 700])
+@pytest.mark.parametrize("a,b", [(30, 0), (0, 40), (60, -60), (-50, 50), (None, None)])
+def test_the_halves_of_a_value_do_not_share_an_operand_scale(a, b, n):
+    """Values whose dims 0..63 and 64..127 differ by up to 2^120 (None: one way and the other, by 32 positions)."""
+    k, v = rows_like_keys(210, n, 1), rows_like_keys(211, n, 1)
+    if a is None:
+        turn = (np.arange(n) // 32 % 2 * 60 - 30)[:, None]
+        v[:, 0, :64] *= (2.0 ** turn).astype(np.float32)
+        v[:, 0, 64:] *= (2.0 ** -turn).astype(np.float32)
+    else:
+        v[..., :64] *= np.float32(2.0 ** a)
+        v[..., 64:] *= np.float32(2.0 ** b)
+    kv = cache_of(k, v)
+    q = queries(212, 3, 8)
+    attn = tfl.KV4Attention(8, 1, max_rows=3, max_positions=n)
+    check(attend(attn, [kv], [n - 3], [3], q), q, range(n - 3, n), ref.quantise(k), ref.quantise(v))
