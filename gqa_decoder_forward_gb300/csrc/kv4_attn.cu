@@ -84,7 +84,7 @@ constexpr int kMaxJoinBytes = (kSpread + kFan - 1) / kFan * kGroupBytes;
 constexpr float kLog2eOverSqrtD = 0.12751743074640502f;
 constexpr float kLazy = 8.f;                   // log2
 constexpr float kUnset = -FLT_MAX;             // m before the first visible key
-constexpr float kTopW = 32768.f;               // w above this moves c
+constexpr float kTopW = 32784.f;               // w above this moves c: those that fp16 rounds to more than 2^15
 constexpr float kLoCode = 16777216.f;          // codes as fp16 numbers: n 2^-24 in bits 0..3,
 constexpr float kHiCode = 1048576.f;           // n 2^-20 in bits 4..7
 
@@ -283,7 +283,7 @@ __device__ __forceinline__ void step(State& e, const Query& q, const char* buf, 
                 // w >= 0: fp16 order is the order of the bits
                 top2 = __vimax3_u16x2(top2, wb[b][0][hk], wb[b][1][hk]);
             }
-        // 2^15 is 0x7800 (a NaN, above it, counts too and stays one)
+        // 2^15 is 0x7800 (a NaN, above it, counts too and stays one); w is above it where it was above kTopW
         move = __any_sync(0xffffffffu, top[0] > e.m[0] + kLazy || top[1] > e.m[1] + kLazy ||
                                            (top2 & 0xffffu) > 0x7800u || top2 > 0x7800ffffu);
     }
@@ -411,7 +411,8 @@ __device__ __forceinline__ void ask_step(char* dst, const char* src, uint64_t* f
 
 // A unit's end, in place: l over the column's lanes, o from code units and c to the
 // output's own scale, the zeros' sums added.  Of the pairs of tiles, the whole bytes
-// less the low codes leave the high ones.
+// less the low codes leave the high ones (with the rounding of both sums: a sixteenth of the low
+// codes' comes into the dim above, 2^-24 relative and less).
 __device__ __forceinline__ void finish(State& e) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

@@ -53,3 +53,31 @@ def test_the_halves_of_a_value_do_not_share_an_operand_scale(a, b, n):
     q = queries(212, 3, 8)
     attn = tfl.KV4Attention(8, 1, max_rows=3, max_positions=n)
     check(attend(attn, [kv], [n - 3], [3], q), q, range(n - 3, n), ref.quantise(k), ref.quantise(v))
+
+
+def test_a_rows_bits_next_to_the_threshold_do_not_depend_on_its_neighbour():
+    """One row's largest weight lies just above 2^15 in operand units, where rounding to fp16 takes it to 2^15, in a step
+    in which the row beside it moves its maximum.  What follows is 2^29 smaller, in dims where all else is 0."""
+    n = 97
+    k, v = np.zeros((n, 1, 128)), np.zeros((n, 1, 128))
+    v[:32, 0, 0] = 15                                   # scale 1, first: operand scale 2^6
+    k[32, 0, 0] = 15 * 2.0 ** -4                        # scale 2^-4
+    v[32, 0, 0] = 15 * 2.0 ** 9                         # scale 2^9, weight 2^(0.1275 x 15 x 2^-12) = 1.00032
+    r = np.random.default_rng(220)
+    v[64:96, 0, 1:64] = 2.0 ** -20 * r.uniform(0, 25, (32, 63))
+    q = np.zeros((2, 1, 128), np.float32)
+    q[0, 0, 0], q[1, 0, 0] = 2.0 ** -8, 100             # the neighbour's score at key 32: 12 above those before
+    k, v = bf16(k), bf16(v)
+    kv = cache_of(k, v)
+    attn = tfl.KV4Attention(1, 1, max_rows=2, max_positions=n)
+    alone = attend(attn, [kv], [95], [1], q[:1])
+    window = attend(attn, [kv], [95], [2], q)
+    assert (window[0] == alone[0]).all()
+    kq, vq = ref.quantise(k), ref.quantise(v)
+    out, bound = ref.attention(q[0].astype(np.float64), 95, kq, vq)
+    # An odd dim's codes are the high halves of bytes: their sum is a sixteenth of the difference of the bytes' sum and the
+    # low codes'.  Both are fp32 sums in chains of at most 64 steps (the restatement's 2^-17 each), so the dim below it,
+    # which alone is large here, adds 2 x 2^-17 / 16 = 2^-20 of its own sum.
+    low, _ = ref.attention(q[0].astype(np.float64), 95, kq, (vq[0], vq[1], 0 * vq[2]))
+    bound[:, 1::2] += 2.0 ** -20 * low[:, 0::2]
+    assert (np.abs(alone[0] - out) <= bound).all()
