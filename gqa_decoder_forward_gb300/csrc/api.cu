@@ -1124,6 +1124,7 @@ int tfl_init(const tfl_config* cfg, const tfl_weights* w, void* workspace, size_
     if (ce == cudaSuccess) ce = cudaMemset(m->status, 0, 256);
     // sampling counts start at zero; every tfl_sample call leaves them zero again
     if (ce == cudaSuccess) ce = cudaMemset(m->scounts, 0, (size_t)cfg->max_decode_rows * 65536 * 4);
+    if (ce == cudaSuccess) ce = cudaStreamSynchronize(cudaStreamLegacy);  // other streams need not wait for it
     if (ce != cudaSuccess) {
         delete m;
         return fail(TFL_E_CUDA, "uploading the RoPE table failed: %s", cudaGetErrorString(ce));
@@ -1197,6 +1198,8 @@ int tfl_kv_alloc(tfl_model* m, int max_positions, void* dev_buf, size_t bytes, t
     std::vector<int> ident(kv->n_pages);
     for (int i = 0; i < kv->n_pages; ++i) ident[i] = i;
     cudaError_t ce = cudaMemcpy(kv->table, ident.data(), ident.size() * 4, cudaMemcpyHostToDevice);
+    // the copy may still be on its way, and streams need not wait for the legacy one
+    if (ce == cudaSuccess) ce = cudaStreamSynchronize(cudaStreamLegacy);
     if (ce != cudaSuccess) {
         delete kv;
         return fail(TFL_E_CUDA, "writing the page table failed: %s", cudaGetErrorString(ce));
@@ -1526,6 +1529,7 @@ int tfl_status(tfl_model* m, void* stream) {
     int s = 0;
     CK(cudaMemcpy(&s, m->status, 4, cudaMemcpyDeviceToHost));
     CK(cudaMemset(m->status, 0, 4));
+    CK(cudaStreamSynchronize(cudaStreamLegacy));
     if (s & kStatusDevice) return fail(TFL_E_DEVICE, "a kernel gave up a bounded wait");
     if (s & kStatusNonFinite) return fail(TFL_E_NONFINITE, "an argmax row held NaN or +-Inf");
     if (s & kStatusBadToken) return fail(TFL_E_ARG, "a token id was outside [0, vocab)");

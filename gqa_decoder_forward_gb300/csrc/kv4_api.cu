@@ -105,6 +105,10 @@ int check_arch(int* dev) {
 // back 4.4 | 3.8 us, one row attending 4,096 keys 8.7 | 8.3 us.
 bool programmatic(void* stream) { return stream != nullptr && stream != (void*)cudaStreamLegacy; }
 
+// Ends what cudaMemcpy and cudaMemset have left to do when they return (a small copy from pageable memory, or a
+// memset, may still be on its way): streams that do not wait for the legacy one find it done.
+cudaError_t settle(cudaError_t e) { return e == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : e; }
+
 bool bad_ptr(const void* p) { return !p || ((uintptr_t)p & 15u); }
 
 bool bad_ld(size_t ld, int heads) { return ld < (size_t)heads * kHeadDim || ld % 8 != 0 || ld > ((size_t)1 << 40); }
@@ -196,7 +200,7 @@ int tfl_kv4_alloc(int layers, int n_kv, int head_dim, int max_positions, void* d
     kv->table = (int*)dev_buf;
     kv->pages = (char*)dev_buf + round256((size_t)n * 4);
     for (int i = 0; i < n; ++i) ident[i] = i;
-    const cudaError_t ce = cudaMemcpy(kv->table, ident, (size_t)n * 4, cudaMemcpyHostToDevice);
+    const cudaError_t ce = settle(cudaMemcpy(kv->table, ident, (size_t)n * 4, cudaMemcpyHostToDevice));
     delete[] ident;
     if (ce != cudaSuccess) {
         delete kv;
@@ -282,7 +286,7 @@ int tfl_kv4_attn_init(int n_q, int n_kv, int head_dim, int max_rows, int max_pos
     a->po = (float*)(ws + L.po);
     a->sms = sms;
     a->status = (int*)(ws + L.status);
-    const cudaError_t ce = cudaMemset(a->status, 0, 256);
+    const cudaError_t ce = settle(cudaMemset(a->status, 0, 256));
     if (ce != cudaSuccess) {
         delete a;
         return fail(TFL_E_CUDA, "clearing the status word failed: %s", cudaGetErrorString(ce));
@@ -297,7 +301,7 @@ int tfl_kv4_attn_status(tfl_kv4_attn* attn, void* stream) {
     int s = 0;
     CK(cudaMemcpy(&s, attn->status, 4, cudaMemcpyDeviceToHost));
     if (s == 0) return ok();
-    CK(cudaMemset(attn->status, 0, 4));
+    CK(settle(cudaMemset(attn->status, 0, 4)));
     return fail(TFL_E_DEVICE, "a kernel gave up a bounded wait");
 }
 

@@ -175,6 +175,13 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _settle():
+    """Ends the work of the current stream.  The library's objects write into their memory when they are made, in no
+    stream's order; a tensor made on the current stream may be the caller's, filled there, or memory that
+    earlier work of the stream still uses."""
+    torch.cuda.current_stream().synchronize()
+
+
 def config(shape, max_rows=64, max_decode_rows=64, max_context=4096) -> tfl_config:
     return tfl_config(shape.hidden, shape.layers, shape.n_q, shape.n_kv, shape.head_dim, shape.ffn, shape.vocab,
                       shape.rope_theta, shape.rms_eps, max_rows, max_decode_rows, max_context)
@@ -228,6 +235,7 @@ class Model:
             setattr(w, k, ctypes.cast(arr, ctypes.POINTER(_vp)))
         self._w = w
         h = _vp()
+        _settle()
         _check(lib().tfl_init(ctypes.byref(self.cfg), ctypes.byref(w), _ptr(self.workspace), nbytes,
                               ctypes.byref(h)))
         self.handle = h
@@ -279,6 +287,7 @@ class KV:
         nbytes = tfl_kv_bytes(model.cfg, max_positions)
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         h = _vp()
+        _settle()
         _check(lib().tfl_kv_alloc(model.handle, int(max_positions), _ptr(self.buffer), nbytes, ctypes.byref(h)))
         self.handle = h
 
@@ -499,6 +508,7 @@ class KV4:
             buffer = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         self.layers, self.n_kv, self.buffer = layers, n_kv, buffer
         h = _vp()
+        _settle()
         _check(lib().tfl_kv4_alloc(layers, n_kv, 128, int(max_positions), _ptr(buffer),
                                    buffer.numel() * buffer.element_size(), ctypes.byref(h)))
         self.handle = h
@@ -552,6 +562,7 @@ class KV4Attention:
         self.n_q, self.n_kv = n_q, n_kv
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device="cuda")
         h = _vp()
+        _settle()
         _check(lib().tfl_kv4_attn_init(n_q, n_kv, 128, max_rows, max_positions, _ptr(self.workspace), nbytes,
                                        ctypes.byref(h)))
         self.handle = h

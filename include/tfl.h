@@ -493,8 +493,10 @@ int tfl_attention_decode_noalloc(tfl_kv* kv, int layer, int pos0, int rows, cons
  * Independent of any model: layers 1..1024, n_kv 1..64 heads, head_dim 128, max_positions
  * 1..2^20.  bytes: 0 for sizes outside these.  tfl_kv4_alloc: dev_buf 16-byte
  * aligned device memory of the current device, owned by the caller and kept
- * alive; writes the page table (synchronously) and nothing else, so a buffer
- * filled before keeps its contents; the length starts at 0.  reset, length and
+ * alive; writes the page table, which is there on return, and nothing else, so a buffer
+ * filled before keeps its contents; the length starts at 0.  The write is not in the
+ * order of any stream: what streams still have to do with the buffer must have ended
+ * (the same holds for tfl_kv4_attn_init and its workspace).  reset, length and
  * capacity as tfl_kv_reset, tfl_kv_length and tfl_kv_capacity.
  */
 #define TFL_KV4_GROUP 64

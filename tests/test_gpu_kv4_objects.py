@@ -1,0 +1,86 @@
+"""Objects of the 4-bit cache made while a stream still works on the memory that they take."""
+import numpy as np
+import pytest
+import torch
+
+from gqa_decoder_forward_gb300 import synth, tfl
+from tests import kv4_ref as ref
+from tests.test_gpu_kv4 import _built, cuda_bf16, put_rows, queries, rows_like_keys  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def busy(stream):
+    """Some tens of milliseconds of ordinary work on a stream, so that what follows it there is late."""
+    x = torch.ones(1 << 28, device="cuda")
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(40):
+            x.add_(1)
+    return x
+
+
+def test_a_cache_over_a_buffer_that_a_side_stream_fills_keeps_its_table():
+    n_kv, cap, n = 2, 500, 300
+    host = ref.Cache(1, n_kv, cap, 0x5A)
+    x, y = rows_like_keys(300, n, n_kv), rows_like_keys(301, n, n_kv)
+    k, v = cuda_bf16(x), cuda_bf16(y)
+    buf = torch.empty(host.bytes.size, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    held = busy(side)
+    with torch.cuda.stream(side):
+        buf.fill_(0x5A)
+        kv = tfl.KV4(1, n_kv, cap, buffer=buf)
+        tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [n]), 0, k, v)
+    torch.cuda.synchronize()
+    del held
+    put_rows(host, 0, 0, 0, x)
+    put_rows(host, 0, 0, 1, y)
+    got = buf.cpu().numpy()
+    assert (got[: host.pages * 4].view(np.int32) == np.arange(host.pages)).all()
+    assert (got[host.table_bytes:] == host.bytes[host.table_bytes:]).all()
+
+
+def test_objects_in_memory_that_a_side_stream_still_writes():
+    """The caching allocator hands a freed block back to its stream while work on it is pending."""
+    kv = tfl.KV4(1, 2, 128)
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [0], [100]), 0, cuda_bf16(rows_like_keys(302, 100, 2)), cuda_bf16(rows_like_keys(303, 100, 2)))
+    q = cuda_bf16(queries(304, 1, 8)).view(1, -1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    nbytes = int(tfl.lib().tfl_kv4_attn_bytes(8, 2, 128, 16, 65536))
+    table = int(tfl.tfl_kv4_bytes(4, 8, 65536))
+    with torch.cuda.stream(side):
+        blocks = [torch.empty(nbytes, dtype=torch.uint8, device="cuda"), torch.empty(table, dtype=torch.uint8, device="cuda")]
+    held = busy(side)
+    with torch.cuda.stream(side):
+        at = [b.data_ptr() for b in blocks]
+        for b in blocks:
+            b.fill_(0xFF)
+        del b, blocks
+        attn = tfl.KV4Attention(8, 2, max_rows=16, max_positions=65536)
+        big = tfl.KV4(4, 8, 65536)
+        out = torch.zeros_like(q)
+        tfl.tfl_kv4_attention(attn, tfl.KV4Rows([kv], [99], [1]), 0, q, out)
+    torch.cuda.synchronize()
+    del held
+    assert at == [attn.workspace.data_ptr(), big.buffer.data_ptr()]   # the blocks that were being written
+    assert tfl.tfl_kv4_attn_status(attn, side) == tfl.TFL_OK
+    assert (big.buffer[: 512 * 4].cpu().numpy().view(np.int32) == np.arange(512)).all()
+    assert torch.isfinite(out.float()).all()
+    # the bf16 cache's table in the same way
+    w = synth.model_weights(synth.TINY, 5, "cuda")
+    m = tfl.Model(synth.TINY, w, max_rows=64, max_decode_rows=4, max_context=4096)
+    size = int(tfl.tfl_kv_bytes(m.cfg, 4096))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        block = torch.empty(size, dtype=torch.uint8, device="cuda")
+    held = busy(side)
+    with torch.cuda.stream(side):
+        where = block.data_ptr()
+        block.fill_(0xFF)
+        del block
+        plain = m.kv(4096)
+    torch.cuda.synchronize()
+    assert where == plain.buffer.data_ptr()
+    assert (plain.buffer[: 32 * 4].cpu().numpy().view(np.int32) == np.arange(32)).all()
