@@ -111,6 +111,9 @@ struct AttnArgs {
     float *pm, *pl, *po;
     int max_units;
     int* status;         // device status word: a bounded wait that gives up raises kStatusDevice
+    bool probe;          // a call in which a wait runs out: of step `lose` of every warp that has it,
+    int lose;            // after wait_limit polls
+    unsigned wait_limit;
 };
 constexpr int kMaxParts = 2 * kMaxStreams;  // attention may cut a call's streams in two
 int attn_max_units(int positions, int n_kv);  // partials of a row's head over caches of up to so many positions

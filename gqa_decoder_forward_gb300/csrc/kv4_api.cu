@@ -161,6 +161,42 @@ int check_rows_tensors(const void* k, const void* v, size_t ld, int n_kv) {
     return TFL_OK;
 }
 
+int attend(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0, const int* rows,
+           const void* q, size_t ldq, void* out, size_t ldo, void* stream, bool probe, int lose, int wait_limit) {
+    if (!attn) return fail(TFL_E_ARG, "NULL attention object");
+    kv4::AttnArgs a;
+    if (int e = fill_rows(a.rows, kvs, n_streams, layer, pos0, rows, kMaxAttnRowsPerStream, false)) return e;
+    if (attn->n_kv != a.rows.n_kv || attn->device != kvs[0]->device)
+        return fail(TFL_E_ARG, "an attention object for %d KV heads on device %d, caches of %d heads on device %d",
+                    attn->n_kv, attn->device, a.rows.n_kv, kvs[0]->device);
+    if (a.rows.n_rows > attn->max_rows)
+        return fail(TFL_E_ARG, "%d rows exceed the object's max_rows %d", a.rows.n_rows, attn->max_rows);
+    for (int s = 0; s < n_streams; ++s)
+        if (rows[s] > 0 && pos0[s] + rows[s] > attn->max_pos)
+            return fail(TFL_E_CAPACITY, "stream %d: positions to %d pass the object's max_positions %d", s,
+                        pos0[s] + rows[s] - 1, attn->max_pos);
+    if (bad_ptr(q) || bad_ptr(out)) return fail(TFL_E_ARG, "q/out NULL or not 16-byte aligned");
+    if (q == out) return fail(TFL_E_ARG, "q and out are the same memory");
+    if (bad_ld(ldq, attn->n_q) || bad_ld(ldo, attn->n_q))
+        return fail(TFL_E_ARG, "ldq %zu / ldo %zu: less than %d heads of %d or not a multiple of 8", ldq, ldo,
+                    attn->n_q, kHeadDim);
+    a.n_q = attn->n_q;
+    a.q = (const bf16*)q;
+    a.ldq = (long)ldq;
+    a.out = (bf16*)out;
+    a.ldo = (long)ldo;
+    a.pm = attn->pm;
+    a.pl = attn->pl;
+    a.po = attn->po;
+    a.max_units = attn->max_units;
+    a.status = attn->status;
+    a.probe = probe;
+    a.lose = lose;
+    a.wait_limit = (unsigned)wait_limit;
+    CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, programmatic(stream)));
+    return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -309,35 +345,16 @@ void tfl_kv4_attn_free(tfl_kv4_attn* attn) { delete attn; }
 
 int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, void* stream) {
-    if (!attn) return fail(TFL_E_ARG, "NULL attention object");
-    kv4::AttnArgs a;
-    if (int e = fill_rows(a.rows, kvs, n_streams, layer, pos0, rows, kMaxAttnRowsPerStream, false)) return e;
-    if (attn->n_kv != a.rows.n_kv || attn->device != kvs[0]->device)
-        return fail(TFL_E_ARG, "an attention object for %d KV heads on device %d, caches of %d heads on device %d",
-                    attn->n_kv, attn->device, a.rows.n_kv, kvs[0]->device);
-    if (a.rows.n_rows > attn->max_rows)
-        return fail(TFL_E_ARG, "%d rows exceed the object's max_rows %d", a.rows.n_rows, attn->max_rows);
-    for (int s = 0; s < n_streams; ++s)
-        if (rows[s] > 0 && pos0[s] + rows[s] > attn->max_pos)
-            return fail(TFL_E_CAPACITY, "stream %d: positions to %d pass the object's max_positions %d", s,
-                        pos0[s] + rows[s] - 1, attn->max_pos);
-    if (bad_ptr(q) || bad_ptr(out)) return fail(TFL_E_ARG, "q/out NULL or not 16-byte aligned");
-    if (q == out) return fail(TFL_E_ARG, "q and out are the same memory");
-    if (bad_ld(ldq, attn->n_q) || bad_ld(ldo, attn->n_q))
-        return fail(TFL_E_ARG, "ldq %zu / ldo %zu: less than %d heads of %d or not a multiple of 8", ldq, ldo,
-                    attn->n_q, kHeadDim);
-    a.n_q = attn->n_q;
-    a.q = (const bf16*)q;
-    a.ldq = (long)ldq;
-    a.out = (bf16*)out;
-    a.ldo = (long)ldo;
-    a.pm = attn->pm;
-    a.pl = attn->pl;
-    a.po = attn->po;
-    a.max_units = attn->max_units;
-    a.status = attn->status;
-    CK(kv4::launch_attn(a, attn->sms, (cudaStream_t)stream, programmatic(stream)));
-    return ok();
+    return attend(attn, kvs, n_streams, layer, pos0, rows, q, ldq, out, ldo, stream, false, 0, 0);
+}
+
+int tfl_kv4_wait_probe(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
+                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, int lose, int spin_limit,
+                       void* stream) {
+    if (lose < 0) return fail(TFL_E_ARG, "step %d", lose);
+    if (spin_limit < 1 || spin_limit > (1 << 20))
+        return fail(TFL_E_ARG, "spin_limit %d outside 1..%d", spin_limit, 1 << 20);
+    return attend(attn, kvs, n_streams, layer, pos0, rows, q, ldq, out, ldo, stream, true, lose, spin_limit);
 }
 
 }  // extern "C"

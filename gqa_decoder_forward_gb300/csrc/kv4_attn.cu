@@ -460,6 +460,8 @@ struct Call {
     long ldo;
     float *pm, *pl, *po;
     int* status;
+    int lose;                             // of a probe: the step that a warp never gets, polls of a wait
+    unsigned wait_limit;
     int start[kMaxParts];                 // a part's first place
     Part part[kMaxParts];
 };
@@ -598,7 +600,7 @@ __device__ __forceinline__ void put_out(const OutRows& o, int d, float4 O, const
 // when the run before it begins, so that no fetch waits for the table.
 struct Fetch {
     const char* next;       // the step to fetch,
-    int run, pad;           // steps left of its run
+    int run, idle;          // steps left of its run; stages that there was no step for
     int page;               // where the table's entry for the run after it arrives:
     int next_run, k, left;  // its steps (0: none), its position, its unit's steps from there on,
     int item, u, nu, unit;  // its unit: place, number, the set's units and their steps,
@@ -607,6 +609,7 @@ struct Fetch {
     const int* table;
     size_t page_bytes;
     unsigned last_page;
+    int asked;              // of a probe: steps asked for
 };
 __device__ __forceinline__ void ask_word(int* dst, const int* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -659,6 +662,9 @@ __device__ __noinline__ void open_run(const Call& a, Fetch* f, int end) {
 
 constexpr int kWarpBytes = (kStages * (kStepBytes + 8) + (int)sizeof(Fetch) + 127) / 128 * 128;  // ring, its barriers, Fetch
 
+// PROBE: every warp that has a step number a.lose announces it and does not copy it, so that the wait
+// for it runs out, after a.wait_limit polls.
+template <bool PROBE>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_constant__ Call a) {
     extern __shared__ __align__(128) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -678,7 +684,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     if (i < end && lane == 0) {
         for (int k = 0; k < kStages; ++k) mbar_init(&full[k], 1);
         mbar_init_fence();
-        f->run = 0;
+        f->run = f->idle = 0;
+        if (PROBE) f->asked = 0;
         open_set(a, f, i, x, u);
     }
     pdl_wait();  // memory from here on
@@ -689,6 +696,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     RawQuery raw;
     ask_query(raw, a, x);  // before the keys, which they would wait behind
     int fslot = 0;
+    auto wait = [&](int slot, uint32_t phase) { return mbar_wait(&full[slot], phase, a.status, PROBE ? a.wait_limit : kMbarSpinLimit); };
+    auto ask = [&](int slot, const char* src) {  // lane 0
+        if (PROBE && f->asked++ == a.lose)
+            mbar_arrive_expect_tx(&full[slot], kStepBytes);
+        else
+            ask_step(buf + slot * kStepBytes, src, &full[slot]);
+    };
     auto fetch = [&]() {
         if (lane == 0) {
             int run = f->run;
@@ -703,9 +717,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
                 }
             }
             if (run > 0) {
-                ask_step(buf + fslot * kStepBytes, src, &full[fslot]);
+                ask(fslot, src);
                 f->next = src + kStepBytes;
                 f->run = run - 1;
+            } else {
+                ++f->idle;
             }
         }
         if (++fslot == kStages) fslot = 0;
@@ -716,7 +732,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             const int run = min(f->left, (kPage - f->k % kPage) / kStepKeys);
             asked = min(run, kStages);
             const char* src = f->heads + min(page0, f->last_page) * f->page_bytes + f->k % kPage / kBlockPos * kBlockBytes;
-            for (int k = 0; k < asked; ++k, src += kStepBytes) ask_step(buf + k * kStepBytes, src, &full[k]);
+            for (int k = 0; k < asked; ++k, src += kStepBytes) ask(k, src);
             f->next = src;
             f->run = run - asked;
             f->k += run * kStepKeys;
@@ -744,7 +760,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
         auto steps = [&](auto edge) {
 #pragma unroll 1
             for (int k = k0; k < k1; k += kStepKeys) {
-                there = there && __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, a.status));
+                there = there && __all_sync(0xffffffffu, wait(slot, phase));
                 if (!there) continue;  // nothing more is asked for
                 step<decltype(edge)::value>(e, q, buf + slot * kStepBytes, k, k == k0);
                 __syncwarp();  // the stage has been read
@@ -789,14 +805,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
             ask_query(raw, a, x);
         }
     }
-    if (!there) {  // the copies in flight end before the CTA does, or these waits run out too
+    if (!there && lane == 0) {  // the copies in flight end before the CTA does, or these waits run out too:
         asm volatile("cp.async.wait_all;" ::: "memory");
-        for (int k = 1; k < kStages; ++k) {
+        for (int k = f->idle; k < kStages; ++k) {  // every stage with a step, from the one that was waited for on
+            wait(slot, phase);
             if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1;
             }
-            mbar_wait(&full[slot], phase, a.status);
         }
     }
 }
@@ -936,7 +952,8 @@ int attn_max_units(int positions, int n_kv) {
 }
 
 cudaError_t init_attn() {
-    cudaError_t e = allow_smem(units_kernel, kWarps * kWarpBytes);
+    cudaError_t e = allow_smem(units_kernel<false>, kWarps * kWarpBytes);
+    if (e == cudaSuccess) e = allow_smem(units_kernel<true>, kWarps * kWarpBytes);
     if (e == cudaSuccess) e = allow_smem(join_kernel, kMaxJoinBytes);
     return e;
 }
@@ -958,6 +975,8 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     c.pl = a.pl;
     c.po = a.po;
     c.status = a.status;
+    c.lose = a.lose;
+    c.wait_limit = a.wait_limit;
     // A stream whose rows lie on both sides of a change of the unit's length (always at a multiple of 32) is
     // two parts.  The work in places where a unit is its steps and one more (its start and end), a set's last
     // unit as long as it is and two more (the set's queries):
@@ -1016,7 +1035,7 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     c.direct = most == 1;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t g = cfg(need < full ? need : full, kWarps * 32, kWarps * kWarpBytes, st, attr, pdl);
-    const cudaError_t e = cudaLaunchKernelEx(&g, units_kernel, c);
+    const cudaError_t e = a.probe ? cudaLaunchKernelEx(&g, units_kernel<true>, c) : cudaLaunchKernelEx(&g, units_kernel<false>, c);
     if (e != cudaSuccess || c.direct) return e;
     const int groups = (most + kFan - 1) / kFan;
     g = cfg(sets * m.n_kv * 8, std::min(groups, sets * m.n_kv * 8 > sms ? kManyJoinWarps : kJoinWarps) * 32,

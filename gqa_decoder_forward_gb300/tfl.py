@@ -123,6 +123,8 @@ SIGNATURES = {
     "tfl_kv4_attn_status": (ctypes.c_int, [_vp, _vp]),
     "tfl_kv4_attention": (ctypes.c_int, [_vp, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
                                          ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
+    "tfl_kv4_wait_probe": (ctypes.c_int, [_vp, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, ctypes.c_size_t, _vp,
+                                          ctypes.c_size_t, ctypes.c_int, ctypes.c_int, _vp]),
     "tfl_kv4_step_workspace_bytes": (ctypes.c_size_t, [_vp]),
     "tfl_decode_step_kv4": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_vp), ctypes.c_int, _vp, _intp, _vp, _vp,
                                            ctypes.c_size_t, _vp]),
@@ -623,6 +625,16 @@ def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.T
     ldo = _rows_arg(out, batch.total, attn.n_q)
     return _check(lib().tfl_kv4_attention(attn.handle, batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at,
                                           q.data_ptr(), ldq, out.data_ptr(), ldo, _stream_of(q, stream)))
+
+
+def tfl_kv4_wait_probe(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.Tensor, out: torch.Tensor, lose: int,
+                       spin_limit: int, stream=None):
+    """tfl_kv4_attention with a copy that never comes: tfl_kv4_attn_status then reports TFL_E_DEVICE."""
+    ldq = _rows_arg(q, batch.total, attn.n_q)
+    ldo = _rows_arg(out, batch.total, attn.n_q)
+    return _check(lib().tfl_kv4_wait_probe(attn.handle, batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at,
+                                           q.data_ptr(), ldq, out.data_ptr(), ldo, lose, spin_limit,
+                                           _stream_of(q, stream)))
 
 
 class KV4Runner:

@@ -566,6 +566,16 @@ int tfl_kv4_attention(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, in
                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, void* stream);
 
 /*
+ * Runs tfl_kv4_attention, whose arguments it takes, with a copy that never comes: every warp that
+ * has a step (32 keys) number `lose` (0: its first) waits for it spin_limit (1..2^20) polls, gives
+ * up, lets its other copies end and returns; tfl_kv4_attn_status then reports TFL_E_DEVICE, if any warp
+ * had that step, and the rows are undefined.  For tests of that path.
+ */
+int tfl_kv4_wait_probe(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
+                       const int* rows, const void* q, size_t ldq, void* out, size_t ldo, int lose, int spin_limit,
+                       void* stream);
+
+/*
  * The forward over 4-bit caches: tfl_decode_step and tfl_prefill_chunk with the
  * keys and values held in caches of the model's layers and KV heads.  Every row,
  * of a step, a window or a chunk, attends what the cache stands for, its own
