@@ -663,9 +663,19 @@ class KV4Runner:
         return tfl_prefill_chunk_kv4(self, kv, ids, logits, all_rows, stream)
 
 
+def _check_ids_and_logits(model: Model, ids, logits, n: int, rows: int):
+    """At least n int32 ids, and bf16 logits (or None) for at least so many rows."""
+    if ids.dtype != torch.int32 or ids.numel() < n:
+        raise ValueError(f"expected {n} int32 ids, got {ids.numel()} of {ids.dtype}")
+    if logits is not None and (logits.dtype != torch.bfloat16 or logits.numel() < rows * model.shape.vocab):
+        raise ValueError(f"expected bf16 logits of {rows} rows of {model.shape.vocab}, got {tuple(logits.shape)} of {logits.dtype}")
+
+
 def tfl_decode_step_kv4(runner: KV4Runner, kvs, ids, rows, logits, stream=None):
-    """tfl_decode_step over 4-bit caches."""
-    assert ids.dtype == torch.int32 and logits.dtype == torch.bfloat16
+    """tfl_decode_step over 4-bit caches: rows[s] ids of each cache, one after the other, to as many rows of logits."""
+    if len(rows) != len(kvs):
+        raise ValueError(f"{len(rows)} row counts for {len(kvs)} caches")
+    _check_ids_and_logits(runner.model, ids, logits, sum(rows), sum(rows))
     r = (ctypes.c_int * len(rows))(*rows)
     return _check(lib().tfl_decode_step_kv4(runner.model.handle, runner.attention.handle, _kv_array(kvs), len(kvs),
                                             _ptr(ids), r, _ptr(logits), _ptr(runner.step_ws), runner.step_ws.numel(),
@@ -673,8 +683,8 @@ def tfl_decode_step_kv4(runner: KV4Runner, kvs, ids, rows, logits, stream=None):
 
 
 def tfl_prefill_chunk_kv4(runner: KV4Runner, kv: KV4, ids, logits=None, all_rows=False, stream=None):
-    """tfl_prefill_chunk into a 4-bit cache."""
-    assert ids.dtype == torch.int32
+    """tfl_prefill_chunk into a 4-bit cache; logits: None, or of the last row, or of all rows."""
+    _check_ids_and_logits(runner.model, ids, logits, 1, ids.numel() if all_rows else 1)
     return _check(lib().tfl_prefill_chunk_kv4(runner.model.handle, kv.handle, _ptr(ids), ids.numel(), _ptr(logits),
                                               1 if all_rows else 0, _ptr(runner.prompt_ws), runner.prompt_ws.numel(),
                                               _stream(stream)))

@@ -1,0 +1,62 @@
+"""What the binding of the 4-bit cache checks before it calls the library (no GPU)."""
+import types
+
+import pytest
+import torch
+
+from gqa_decoder_forward_gb300 import build, tfl
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+VOCAB = 40
+
+
+def runner():
+    """Stands for a KV4Runner without a model: the library refuses its NULL handles."""
+    null = types.SimpleNamespace(handle=None, shape=types.SimpleNamespace(vocab=VOCAB))
+    ws = torch.empty(0, dtype=torch.uint8)
+    return types.SimpleNamespace(model=null, attention=null, step_ws=ws, prompt_ws=ws)
+
+
+def caches(n):
+    return [types.SimpleNamespace(handle=None)] * n
+
+
+def ids(n, dtype=torch.int32):
+    return torch.zeros(n, dtype=dtype)
+
+
+def logits(n, dtype=torch.bfloat16):
+    return torch.zeros(n, VOCAB, dtype=dtype)
+
+
+@pytest.mark.parametrize("kvs,i,rows,out", [
+    (2, ids(2), [1], logits(2)),                       # the row counts end before the caches
+    (1, ids(2), [1, 1], logits(2)),
+    (2, ids(4), [2, 3], logits(5)),                    # fewer ids than rows
+    (2, ids(5), [2, 3], logits(4)),                    # fewer rows of logits
+    (1, ids(1, torch.int64), [1], logits(1)),
+    (1, ids(1), [1], logits(1, torch.float32)),
+])
+def test_a_step_checks_the_lengths_of_its_arrays(kvs, i, rows, out):
+    with pytest.raises(ValueError):
+        tfl.tfl_decode_step_kv4(runner(), caches(kvs), i, rows, out, stream=0)
+
+
+@pytest.mark.parametrize("i,out,all_rows", [(ids(3), logits(2), True), (ids(3), logits(0), False), (ids(0), None, False),
+                                            (ids(3, torch.int64), None, False), (ids(3), logits(3, torch.float32), True)])
+def test_a_prompt_chunk_checks_its_ids_and_logits(i, out, all_rows):
+    with pytest.raises(ValueError):
+        tfl.tfl_prefill_chunk_kv4(runner(), caches(1)[0], i, out, all_rows, stream=0)
+
+
+def test_lengths_that_fit_reach_the_library():
+    for call, args in ((tfl.tfl_decode_step_kv4, (caches(2), ids(6), [2, 3], logits(5))),
+                       (tfl.tfl_prefill_chunk_kv4, (caches(1)[0], ids(3), logits(1), False))):
+        with pytest.raises(tfl.TflError) as e:
+            call(runner(), *args, stream=0)
+        assert e.value.code == tfl.TFL_E_ARG
