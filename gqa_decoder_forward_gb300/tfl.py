@@ -508,6 +508,8 @@ class KV4:
         nbytes = tfl_kv4_bytes(layers, n_kv, max_positions)
         if buffer is None:
             buffer = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        if not buffer.is_cuda or not buffer.is_contiguous() or buffer.get_device() != torch.cuda.current_device():
+            raise ValueError(f"expected a contiguous buffer on the current device, got strides {buffer.stride()} on {buffer.device}")
         self.layers, self.n_kv, self.buffer = layers, n_kv, buffer
         h = _vp()
         _settle()
@@ -540,6 +542,7 @@ class KV4Rows:
     def __init__(self, kvs: Sequence[KV4], pos0: Sequence[int], rows: Sequence[int]):
         self.kvs = list(kvs)
         self.n = len(self.kvs)
+        self.device = self.kvs[0].buffer.get_device() if self.kvs else -1
         self.handles = (_vp * self.n)(*[kv.handle for kv in self.kvs])
         self.pos0 = (ctypes.c_int * self.n)()
         self.rows = (ctypes.c_int * self.n)()
@@ -579,11 +582,12 @@ def tfl_kv4_attn_status(attn: KV4Attention, stream=None) -> int:
     return int(lib().tfl_kv4_attn_status(attn.handle, _stream(stream)))
 
 
-def _rows_arg(t: torch.Tensor, n: int, heads: int) -> int:
-    """Row stride (elements) of a bf16 CUDA tensor of at least n rows of heads x 128
-    numbers, [rows, heads, 128] or [rows, heads * 128]; only rows may be strided."""
-    if t.dtype is not torch.bfloat16 or not t.is_cuda:
-        raise ValueError("expected a bf16 CUDA tensor")
+def _rows_arg(t: torch.Tensor, batch: KV4Rows, heads: int) -> int:
+    """Row stride (elements) of a bf16 CUDA tensor, on the caches' device, of at least the
+    batch's rows of heads x 128 numbers, [rows, heads, 128] or [rows, heads * 128]; only rows may be strided."""
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.get_device() != batch.device:
+        raise ValueError(f"expected a bf16 tensor on CUDA device {batch.device}")
+    n = batch.total
     sh, st = t.shape, t.stride()
     if len(sh) == 2:
         ok = sh[1] == heads * 128 and st[1] == 1
@@ -602,8 +606,8 @@ def _stream_of(t: torch.Tensor, stream) -> int:
 
 def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
     """Quantises rows k, v into the caches of batch."""
-    ld = _rows_arg(k, batch.total, batch.n_kv)
-    if _rows_arg(v, batch.total, batch.n_kv) != ld:
+    ld = _rows_arg(k, batch, batch.n_kv)
+    if _rows_arg(v, batch, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
     return _check(lib().tfl_kv4_write(batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at, k.data_ptr(),
                                       v.data_ptr(), ld, _stream_of(k, stream)))
@@ -611,8 +615,8 @@ def tfl_kv4_write(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, 
 
 def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None):
     """Reads what the caches of batch stand for into k, v."""
-    ld = _rows_arg(k, batch.total, batch.n_kv)
-    if _rows_arg(v, batch.total, batch.n_kv) != ld:
+    ld = _rows_arg(k, batch, batch.n_kv)
+    if _rows_arg(v, batch, batch.n_kv) != ld:
         raise ValueError("k and v have different row strides")
     return _check(lib().tfl_kv4_read(batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at, k.data_ptr(),
                                      v.data_ptr(), ld, _stream_of(k, stream)))
@@ -621,8 +625,8 @@ def tfl_kv4_read(batch: KV4Rows, layer: int, k: torch.Tensor, v: torch.Tensor, s
 def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.Tensor, out: torch.Tensor,
                       stream=None):
     """Attention of the rows q over the caches of batch (which hold those rows' own keys and values)."""
-    ldq = _rows_arg(q, batch.total, attn.n_q)
-    ldo = _rows_arg(out, batch.total, attn.n_q)
+    ldq = _rows_arg(q, batch, attn.n_q)
+    ldo = _rows_arg(out, batch, attn.n_q)
     return _check(lib().tfl_kv4_attention(attn.handle, batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at,
                                           q.data_ptr(), ldq, out.data_ptr(), ldo, _stream_of(q, stream)))
 
@@ -630,8 +634,8 @@ def tfl_kv4_attention(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.T
 def tfl_kv4_wait_probe(attn: KV4Attention, batch: KV4Rows, layer: int, q: torch.Tensor, out: torch.Tensor, lose: int,
                        spin_limit: int, stream=None):
     """tfl_kv4_attention with a copy that never comes: tfl_kv4_attn_status then reports TFL_E_DEVICE."""
-    ldq = _rows_arg(q, batch.total, attn.n_q)
-    ldo = _rows_arg(out, batch.total, attn.n_q)
+    ldq = _rows_arg(q, batch, attn.n_q)
+    ldo = _rows_arg(out, batch, attn.n_q)
     return _check(lib().tfl_kv4_wait_probe(attn.handle, batch.handles_at, batch.n, layer, batch.pos0_at, batch.rows_at,
                                            q.data_ptr(), ldq, out.data_ptr(), ldo, lose, spin_limit,
                                            _stream_of(q, stream)))
@@ -663,19 +667,23 @@ class KV4Runner:
         return tfl_prefill_chunk_kv4(self, kv, ids, logits, all_rows, stream)
 
 
-def _check_ids_and_logits(model: Model, ids, logits, n: int, rows: int):
-    """At least n int32 ids, and bf16 logits (or None) for at least so many rows."""
+def _check_ids_and_logits(runner: KV4Runner, ids, logits, n: int, rows: int):
+    """At least n int32 ids, and bf16 logits (or None) for at least so many rows, on the runner's device."""
+    vocab = runner.model.shape.vocab
+    for t in (ids, logits):
+        if t is not None and t.get_device() != runner.step_ws.get_device():
+            raise ValueError(f"expected ids and logits on {runner.step_ws.device}, got {t.device}")
     if ids.dtype != torch.int32 or ids.numel() < n:
         raise ValueError(f"expected {n} int32 ids, got {ids.numel()} of {ids.dtype}")
-    if logits is not None and (logits.dtype != torch.bfloat16 or logits.numel() < rows * model.shape.vocab):
-        raise ValueError(f"expected bf16 logits of {rows} rows of {model.shape.vocab}, got {tuple(logits.shape)} of {logits.dtype}")
+    if logits is not None and (logits.dtype != torch.bfloat16 or logits.numel() < rows * vocab):
+        raise ValueError(f"expected bf16 logits of {rows} rows of {vocab}, got {tuple(logits.shape)} of {logits.dtype}")
 
 
 def tfl_decode_step_kv4(runner: KV4Runner, kvs, ids, rows, logits, stream=None):
     """tfl_decode_step over 4-bit caches: rows[s] ids of each cache, one after the other, to as many rows of logits."""
     if len(rows) != len(kvs):
         raise ValueError(f"{len(rows)} row counts for {len(kvs)} caches")
-    _check_ids_and_logits(runner.model, ids, logits, sum(rows), sum(rows))
+    _check_ids_and_logits(runner, ids, logits, sum(rows), sum(rows))
     r = (ctypes.c_int * len(rows))(*rows)
     return _check(lib().tfl_decode_step_kv4(runner.model.handle, runner.attention.handle, _kv_array(kvs), len(kvs),
                                             _ptr(ids), r, _ptr(logits), _ptr(runner.step_ws), runner.step_ws.numel(),
@@ -684,7 +692,7 @@ def tfl_decode_step_kv4(runner: KV4Runner, kvs, ids, rows, logits, stream=None):
 
 def tfl_prefill_chunk_kv4(runner: KV4Runner, kv: KV4, ids, logits=None, all_rows=False, stream=None):
     """tfl_prefill_chunk into a 4-bit cache; logits: None, or of the last row, or of all rows."""
-    _check_ids_and_logits(runner.model, ids, logits, 1, ids.numel() if all_rows else 1)
+    _check_ids_and_logits(runner, ids, logits, 1, ids.numel() if all_rows else 1)
     return _check(lib().tfl_prefill_chunk_kv4(runner.model.handle, kv.handle, _ptr(ids), ids.numel(), _ptr(logits),
                                               1 if all_rows else 0, _ptr(runner.prompt_ws), runner.prompt_ws.numel(),
                                               _stream(stream)))

@@ -60,3 +60,45 @@ def test_lengths_that_fit_reach_the_library():
         with pytest.raises(tfl.TflError) as e:
             call(runner(), *args, stream=0)
         assert e.value.code == tfl.TFL_E_ARG
+
+
+def test_a_cache_takes_memory_of_the_current_device_alone():
+    n = tfl.tfl_kv4_bytes(1, 1, 128)
+    with pytest.raises(ValueError):
+        tfl.KV4(1, 1, 128, buffer=torch.empty(n, dtype=torch.uint8))     # the host's
+    with pytest.raises(ValueError):
+        tfl.KV4(1, 1, 128, buffer=torch.empty(2 * n, dtype=torch.uint8)[::2])
+
+
+def rows_on(device, heads=2, rows=3):
+    """Stands for a bf16 CUDA tensor [rows, heads, 128] of a device."""
+    return types.SimpleNamespace(dtype=torch.bfloat16, is_cuda=True, shape=(rows, heads, 128),
+                                 stride=lambda: (heads * 128, 128, 1), get_device=lambda: device, data_ptr=lambda: 256)
+
+
+def cache_on(device, n_kv=2):
+    return types.SimpleNamespace(handle=None, n_kv=n_kv, buffer=types.SimpleNamespace(get_device=lambda: device))
+
+
+def test_rows_of_another_device_than_the_caches_are_refused():
+    batch = tfl.KV4Rows([cache_on(0)], [0], [3])
+    attn = types.SimpleNamespace(handle=None, n_q=2)
+    here, there = rows_on(0), rows_on(1)
+    for call in (tfl.tfl_kv4_write, tfl.tfl_kv4_read):
+        for k, v in ((here, there), (there, here), (there, there)):
+            with pytest.raises(ValueError):
+                call(batch, 0, k, v, stream=0)
+        with pytest.raises(tfl.TflError):                                # the library, of the NULL cache
+            call(batch, 0, here, here, stream=0)
+    for q, out in ((here, there), (there, here)):
+        with pytest.raises(ValueError):
+            tfl.tfl_kv4_attention(attn, batch, 0, q, out, stream=0)
+
+
+def test_ids_or_logits_of_another_device_are_refused():
+    r = runner()
+    r.step_ws = types.SimpleNamespace(get_device=lambda: 0, device="cuda:0")
+    with pytest.raises(ValueError):
+        tfl.tfl_decode_step_kv4(r, caches(1), ids(1), [1], logits(1), stream=0)
+    with pytest.raises(ValueError):
+        tfl.tfl_prefill_chunk_kv4(r, caches(1)[0], ids(1), logits(1), False, stream=0)
