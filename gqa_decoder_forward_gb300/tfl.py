@@ -11,6 +11,7 @@ and nothing here falls back to another implementation.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Sequence
 
@@ -552,6 +553,9 @@ class KV4Rows:
     def set(self, pos0: Sequence[int], rows: Sequence[int]):
         if len(pos0) != self.n or len(rows) != self.n:
             raise ValueError(f"{len(pos0)} positions and {len(rows)} row counts for {self.n} caches")
+        pos0, rows = list(map(operator.index, pos0)), list(map(operator.index, rows))
+        if not all(-2 ** 31 <= x < 2 ** 31 for x in pos0 + rows):  # an int array would keep their low halves
+            raise ValueError(f"positions {pos0} or row counts {rows} outside 32 bits")
         self.pos0[:] = pos0
         self.rows[:] = rows
         self.total = sum(rows)

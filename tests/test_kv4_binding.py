@@ -102,3 +102,13 @@ def test_ids_or_logits_of_another_device_are_refused():
         tfl.tfl_decode_step_kv4(r, caches(1), ids(1), [1], logits(1), stream=0)
     with pytest.raises(ValueError):
         tfl.tfl_prefill_chunk_kv4(r, caches(1)[0], ids(1), logits(1), False, stream=0)
+
+
+@pytest.mark.parametrize("pos0,rows", [([2 ** 32 + 3], [1]), ([3], [2 ** 32 + 1]), ([-2 ** 31 - 1], [1]), ([5.0], [1]), ([5], [1.0])])
+def test_positions_and_rows_that_no_int_holds_are_refused_and_change_nothing(pos0, rows):
+    with pytest.raises((ValueError, TypeError)):
+        tfl.KV4Rows([cache_on(0)], pos0, rows)
+    batch = tfl.KV4Rows([cache_on(0)], [1], [2])
+    with pytest.raises((ValueError, TypeError)):
+        batch.set(pos0, rows)
+    assert (list(batch.pos0), list(batch.rows), batch.total) == ([1], [2], 2)
