@@ -65,8 +65,32 @@ __device__ __forceinline__ int stream_of(const Rows& m, int r) {
     return s;
 }
 
+// Loads of what the kernel before may have written.  A kernel is set up while that one still runs, so
+// its memory is not read-only for the kernel's life, which the read-only path (ld.global.nc) asks for: such a load
+// could be moved before pdl_wait.  These stay behind it (volatile, as it is).
+__device__ __forceinline__ uint32_t load_word(const void* p) {
+    uint32_t x;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(x) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ uint32_t load_once(const void* p) {  // not to be kept in the caches
+    uint32_t x;
+    asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(x) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ float load_l2(const float* p) {
+    float x;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ float4 load_l2(const float4* p) {
+    float4 x;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+    return x;
+}
+
 // The physical page of pos: below v.n_pages in a sound table.
-__device__ __forceinline__ unsigned page_of(const View& v, int pos) { return (unsigned)__ldg(v.table + pos / kPage); }
+__device__ __forceinline__ unsigned page_of(const View& v, int pos) { return load_word(v.table + pos / kPage); }
 
 // The tile of (layer, page, head); of an entry outside the cache, one of the last page's.
 __device__ __forceinline__ char* tile(const View& v, int layer, int n_kv, unsigned page, int head) {

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) units_kernel(const __grid_
     pdl_trigger();
     if (i >= end) return;  // no unit starts in the share
 
-    const unsigned page0 = __ldg(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
+    const unsigned page0 = load_word(a.part[x.p].table + min(u * x.unit * kStepKeys, x.last) / kPage);
     RawQuery raw;
     ask_query(raw, a, x);  // before the keys, which they would wait behind
     int fslot = 0;
@@ -829,11 +829,11 @@ __device__ __forceinline__ void join(const float* pm, const float* pl, const flo
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
         const bool in = 4 * r + a < n;
-        m[r] = in ? __ldcg(pm + (4 * r + a) * 8 + c) : kUnset;
-        l[r] = in ? __ldcg(pl + (4 * r + a) * 8 + c) : 0.f;
+        m[r] = in ? load_l2(pm + (4 * r + a) * 8 + c) : kUnset;
+        l[r] = in ? load_l2(pl + (4 * r + a) * 8 + c) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < kFan; ++i) v[i] = __ldcg(po + min(i, n - 1) * 256);  // past n: weight 0 below
+    for (int i = 0; i < kFan; ++i) v[i] = load_l2(po + min(i, n - 1) * 256);  // past n: weight 0 below
     float top = m[0];
 #pragma unroll
     for (int r = 1; r < kR; ++r) top = fmaxf(top, m[r]);

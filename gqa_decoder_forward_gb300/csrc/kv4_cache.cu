@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // rows i * 2 + half: what was never written is read but not used
         const int r = 2 * i + half;
-        code[i] = __ldcs(reinterpret_cast<const uint32_t*>(hb + word_at(r, c, j)));
-        meta[i] = __ldg(reinterpret_cast<const uint32_t*>(hb + kMetaOff + r * kMetaBytes + j * 4));
+        code[i] = load_once(hb + word_at(r, c, j));
+        meta[i] = load_word(hb + kMetaOff + r * kMetaBytes + j * 4);
     }
     bf16* out = (kind ? a.v : a.k) + (long)h * kHeadDim + j * 64 + c * 8;
 #pragma unroll
