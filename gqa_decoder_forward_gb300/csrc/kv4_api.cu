@@ -175,6 +175,7 @@ int attend(tfl_kv4_attn* attn, tfl_kv4* const* kvs, int n_streams, int layer, co
         if (rows[s] > 0 && pos0[s] + rows[s] > attn->max_pos)
             return fail(TFL_E_CAPACITY, "stream %d: positions to %d pass the object's max_positions %d", s,
                         pos0[s] + rows[s] - 1, attn->max_pos);
+    if (a.rows.n_rows == 0) return ok();  // whatever the tensors
     if (bad_ptr(q) || bad_ptr(out)) return fail(TFL_E_ARG, "q/out NULL or not 16-byte aligned");
     if (q == out) return fail(TFL_E_ARG, "q and out are the same memory");
     if (bad_ld(ldq, attn->n_q) || bad_ld(ldo, attn->n_q))
@@ -262,6 +263,7 @@ int tfl_kv4_write(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0
                   const void* v, size_t ld, void* stream) {
     kv4::WriteArgs a;
     if (int e = fill_rows(a.rows, kvs, n_streams, layer, pos0, rows, 0, true)) return e;
+    if (a.rows.n_rows == 0) return ok();  // whatever the tensors
     if (int e = check_rows_tensors(k, v, ld, a.rows.n_kv)) return e;
     a.k = (const bf16*)k;
     a.v = (const bf16*)v;
@@ -275,6 +277,7 @@ int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
                  size_t ld, void* stream) {
     kv4::ReadArgs a;
     if (int e = fill_rows(a.rows, kvs, n_streams, layer, pos0, rows, 0, false)) return e;
+    if (a.rows.n_rows == 0) return ok();  // whatever the tensors
     if (int e = check_rows_tensors(k, v, ld, a.rows.n_kv)) return e;
     if (k == v) return fail(TFL_E_ARG, "k and v are the same memory");
     a.k = (bf16*)k;

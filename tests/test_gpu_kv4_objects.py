@@ -84,3 +84,17 @@ def test_objects_in_memory_that_a_side_stream_still_writes():
     torch.cuda.synchronize()
     assert where == plain.buffer.data_ptr()
     assert (plain.buffer[: 32 * 4].cpu().numpy().view(np.int32) == np.arange(32)).all()
+
+
+def test_calls_without_rows_take_empty_tensors():
+    kv = tfl.KV4(1, 2, 128)
+    before = kv.buffer.clone()
+    attn = tfl.KV4Attention(8, 2, max_rows=1, max_positions=128)
+    none = tfl.KV4Rows([kv, kv], [3, 9], [0, 0])
+    k, v = (torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [3], [0]), 0, k, v)
+    tfl.tfl_kv4_read(none, 0, k, v)
+    q = torch.empty((0, 8 * 128), dtype=torch.bfloat16, device="cuda")
+    tfl.tfl_kv4_attention(attn, none, 0, q, torch.empty_like(q))
+    torch.cuda.synchronize()
+    assert torch.equal(kv.buffer, before)
