@@ -599,7 +599,7 @@ def _rows_arg(t: torch.Tensor, batch: KV4Rows, heads: int) -> int:
         ok = len(sh) == 3 and sh[1] == heads and sh[2] == 128 and st[2] == 1 and (heads == 1 or st[1] == 128)
     if not ok or sh[0] < n:
         raise ValueError(f"expected [>= {n}, {heads} * 128] with contiguous rows, got {tuple(sh)} strides {st}")
-    return st[0] if sh[0] > 1 else heads * 128
+    return st[0] if n > 1 else heads * 128  # of one row, whatever its tensor's stride
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:

@@ -98,3 +98,14 @@ def test_calls_without_rows_take_empty_tensors():
     tfl.tfl_kv4_attention(attn, none, 0, q, torch.empty_like(q))
     torch.cuda.synchronize()
     assert torch.equal(kv.buffer, before)
+
+
+def test_one_row_of_tensors_with_different_strides():
+    kv, twin = tfl.KV4(1, 2, 128), tfl.KV4(1, 2, 128)
+    kv.buffer[256:].zero_(), twin.buffer[256:].zero_()
+    k, v = (cuda_bf16(rows_like_keys(s, 1, 2)) for s in (310, 311))
+    wide = torch.zeros((4, 3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    wide[:1, 1] = v
+    tfl.tfl_kv4_write(tfl.KV4Rows([kv], [7], [1]), 0, k, wide[:, 1])
+    tfl.tfl_kv4_write(tfl.KV4Rows([twin], [7], [1]), 0, k, v)
+    assert torch.equal(kv.buffer, twin.buffer)

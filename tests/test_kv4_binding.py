@@ -112,3 +112,12 @@ def test_positions_and_rows_that_no_int_holds_are_refused_and_change_nothing(pos
     with pytest.raises((ValueError, TypeError)):
         batch.set(pos0, rows)
     assert (list(batch.pos0), list(batch.rows), batch.total) == ([1], [2], 2)
+
+
+def test_one_row_may_be_a_tensor_of_one_row_beside_a_part_of_wider_rows():
+    one, wide = rows_on(0, rows=1), rows_on(0, rows=5)
+    wide.stride = lambda: (5 * 256, 128, 1)
+    with pytest.raises(tfl.TflError):                                    # the library, of the NULL cache
+        tfl.tfl_kv4_write(tfl.KV4Rows([cache_on(0)], [0], [1]), 0, one, wide, stream=0)
+    with pytest.raises(ValueError):
+        tfl.tfl_kv4_write(tfl.KV4Rows([cache_on(0)], [0], [2]), 0, rows_on(0), wide, stream=0)
