@@ -102,7 +102,7 @@ int check_arch(int* dev) {
 // A call's first kernel may be set up while the stream's last one ends (every kernel here
 // waits for that end before it touches memory).  Not on the legacy stream, which also
 // waits for other streams.  Call after call without | with it: one token written and read
-// back 4.4 | 3.8 us, one row attending 4,096 keys 8.7 | 8.3 us.
+// back 4.3 | 3.5 us, one row attending 4,096 keys 8.6 | 8.2 us.
 bool programmatic(void* stream) { return stream != nullptr && stream != (void*)cudaStreamLegacy; }
 
 // Ends what cudaMemcpy and cudaMemset have left to do when they return (a small copy from pageable memory, or a

@@ -16,8 +16,9 @@
 // are fp32.
 //
 // The weights' operand is w = fp16(P s c), c a power of two per column and group: one rounding
-// of 2^-11 relative, far below the output's 2^-8, at half the tensor work of a split
-// into two numbers.  c is set, up or down, so that the largest w of 32 keys is 2^6..2^7:
+// of 2^-11 relative, below the output's 2^-8, at half the tensor work of a split into two
+// numbers.  The sum over the zeros takes P unrounded, so the error goes with P s n and a dim
+// that stands for exact zeros stays exact.  c is set, up or down, so that the largest w of 32 keys is 2^6..2^7:
 // at a unit's start, whenever m moves (which makes what came before smaller), and when a w
 // passes 2^15; the running output moves with it.  So products P s down to 2^-20 of the group's
 // largest keep fp16's full 11 bits and smaller ones an absolute 2^-31 of it.  m moves only
@@ -58,12 +59,15 @@ constexpr int kStepBytes = 2 * kBlockBytes;        // 4,608
 // Steps of a unit, by the position of the row that attends and the cache's heads:
 // as long as that leaves every warp of a full grid at most one unit, but not below a
 // shortest: more steps mean fewer starts and partials, fewer mean more warps for one short
-// cache.  8 KV heads, seven query heads each.  Shortest before position 8,192, with 3 | 4 | 5 |
-// 6 | 8 steps: one row over 4,096 keys 7.9 | 8.1 | 9.0 | 9.7 | 11.2 us, 16 rows over up to
-// 8,192 each 33.6 | 31.1 | 33.4 | 29.7 | 33.4 us.  From there on, with 6 | 8 | 10 | 12: one row
-// over 9,000 keys 12.2 | 13.3 | 15.4 | 17.3 us, rows over 1 to 32,000 keys 47.6 | 45.2 | 42.8 |
-// 43.5 us, a window of 16 rows over 20,000 89 | 81 | 79 | 85 us.  One row over 131,072 keys with
-// 8 steps, two or three units to a warp: 43 us, with 18 and one unit: 34 us.
+// cache.  8 KV heads, seven query heads each, graph replays.  Shortest before position 8,192,
+// with 3 | 4 | 5 | 6 | 8 steps: one row over 4,096 keys 8.1 | 8.2 | 9.0 | 9.8 | 11.2 us, 16 rows
+// over up to 8,192 each 33.9 | 31.4 | 34.0 | 30.3 | 33.8 us, a window of 16 rows over 4,096 26.1 |
+// 24.1 | 23.6 | 23.4 | 25.1 us (1 KV head, one row over 4,096: 8.1 | 7.8 | 8.6 | 9.5 | 10.9 us; 64
+// of one query each, 16 rows over up to 8,192: 174 | 174 | 173 | 174 | 170 us).  From there on, with
+// 6 | 8 | 10 | 12: one row over 9,000 keys 11.4 | 11.7 | 13.1 | 14.6 us, rows over 1 to 32,000 keys
+// 47.2 | 45.2 | 42.6 | 42.9 us, a window of 16 rows over 20,000 75.8 | 68.4 | 66.8 | 72.1 us (1 KV
+// head, one row over 131,072: 19.3 | 17.1 | 17.8 | 18.3 us).  One row over 131,072 keys of 8 heads with
+// 8 steps, two or three units to a warp: 43.9 us, with 18 and one unit: 34.1 us.
 constexpr int kSpread = 152 * 12;                  // warps of the full grid
 __host__ inline int unit_steps(int pos, int n_kv) {
     const int most = kSpread / n_kv, steps = pos / kStepKeys + 1;
@@ -71,13 +75,14 @@ __host__ inline int unit_steps(int pos, int n_kv) {
 }
 constexpr int kWarps = 4;                          // of a CTA
 // CTAs of an SM and steps of a warp's ring.  168 registers a thread allow three CTAs (four, at
-// 128, spill).  16 rows over up to 8,192 keys each with rings of 2 | 3 | 4: 31.6 | 33.1 | 35.8 us,
-// with two CTAs and rings of 4 | 6: 37.4 | 39.9 us.
+// 128, spill).  16 rows over up to 8,192 keys each with rings of 2 | 3 | 4: 31.4 | 32.7 | 35.8 us,
+// with two CTAs and rings of 4 | 6: 38.3 | 39.9 us.
 constexpr int kCtas = 3, kStages = 2;
 constexpr int kFan = 8;                           // units joined at a time
-// Warps of a CTA of the join, on a grid of at most a CTA per SM, or more.  16 rows over up to
-// 8,192 keys with 4 | 16: 32.9 | 35.3 us (groups of 16 units, 2 | 16 warps: 32.6 | 34.2 us; a
-// window of 16 rows over 4,096 keys prefers 8: 24.5 against 25.3 us).
+// Warps of a CTA of the join, on a grid of at most a CTA per SM, or more.  On the larger ones with
+// 2 | 4 | 8 | 16: 16 rows over up to 8,192 keys 33.0 | 31.4 | 33.2 | 33.3 us, rows over 1 to 32,000
+// 53.7 | 45.2 | 45.5 | 48.6 us, a window of 16 rows over 4,096 24.7 | 24.1 | 23.2 | 23.3 us (groups of 16
+// units, 2 | 4 | 16 warps: the first 31.5 | 33.2 | 33.1 us).
 constexpr int kJoinWarps = 16, kManyJoinWarps = 4;
 constexpr int kGroupBytes = 36 * 16;               // a joined group: 32 float4, eight maxima, eight sums
 constexpr int kMaxJoinBytes = (kSpread + kFan - 1) / kFan * kGroupBytes;
@@ -918,7 +923,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         return;
     }
     // Only now: set up earlier, the next kernel's CTAs take the place of joins that have not begun.
-    // 16 rows over up to 8,192 keys, call after call: 34.1 us, with a trigger at the top 39.7.
+    // 16 rows over up to 8,192 keys, call after call: 31.4 us, with a trigger at the top 38.0 (one row
+    // over 4,096 keys 8.2 | 7.6, over 131,072 34.1 | 33.0).
     pdl_trigger();
     const float inv[2] = {1.f / L[0], 1.f / L[1]};
     put_out(out_rows(a, x), d, O, inv);
@@ -1013,8 +1019,8 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st, bool pdl) {
     c.n_parts = n;
     // As many warps as there are units, one each, or a full grid whose warps share the places; or the units,
     // if all have the same steps and that leaves the warp with the most work less.  By
-    // units | by places: 16 rows over up to 8,192 keys 35.0 | 38.2 us, 16 rows of one stream over 4,096 keys
-    // 26.8 | 25.9 us.
+    // units | by places: 16 rows over up to 8,192 keys 31.4 | 32.4 us, 16 rows of one stream over 4,096 keys,
+    // which the rule shares by places, 23.4 | 24.1 us, rows over 1 to 32,000 keys 45.6 | 45.2 us.
     const int full = sms * kCtas, need = (units + kWarps - 1) / kWarps, warps = full * kWarps;
     c.per_sm = need < full ? 1 : kCtas;
     bool count = need <= full;

@@ -1,17 +1,16 @@
 // Writing rows into the 4-bit cache and reading them back (layout and formula:
-// kv4.cuh).  Both are bound by the bytes of the dense side (256 of a row of 128 bf16
-// numbers against 72 held), so a lane moves 16 dense bytes at a time and keeps
-// several rows in flight.
+// kv4.cuh).  Most of the bytes are the dense side's (256 of a row of 128 bf16
+// numbers against 72 held), of which a lane moves 16 at a time.
 //
 // Write: sixteen lanes take a head's key or value of a row: a lane loads eight bf16
 // numbers, eight lanes find their group's minimum and maximum by shuffles, and each
 // lane writes one 32-bit word of codes.  One token costs a launch (1.8 us in a graph);
-// 2,048 rows of 8 heads (10.7 MB, 1.6 us of transfer) some 6 us: 300 instructions of a
-// warp for four such row-heads, two in five of them on the half-rate pipes.  Key and
-// value in one lane share the index work but cost one token 0.7 us more.
+// 2,048 rows of 8 heads (10.7 MB, 1.6 us of transfer) some 6 us: 303 instructions of a
+// warp for two such row-heads, two in five of them on the half-rate pipes, and one load of a
+// lane in flight.  Key and value in one lane share the index work but cost one token 0.7 us more.
 // Read: a warp takes 16 positions of a block (1,152 contiguous bytes of the cache,
-// half a block), a half warp a row at a time; a lane holds one word of eight rows.
-// 131,072 positions of 8 heads (688 MB): 101-102 us, 6.8 TB/s, what a copy takes; 8,192
+// half a block), a half warp a row at a time; a lane holds one word of eight rows, all in flight.
+// 131,072 positions of 8 heads (688 MB): 101 us, 6.8 TB/s, what a copy takes; 8,192
 // positions (43 MB): 8.7 us, 4.9 TB/s, the rest being launch and ramp.  (A warp per row:
 // 196 us for the former.)
 #include "kv4.cuh"

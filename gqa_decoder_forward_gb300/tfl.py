@@ -503,7 +503,9 @@ def tfl_kv4_bytes(layers: int, n_kv: int, max_positions: int, head_dim: int = 12
 
 class KV4:
     """A paged cache in 4 bits (tfl_kv4) over `buffer` (a uint8 CUDA tensor of at
-    least tfl_kv4_bytes bytes, whose contents are kept) or one that it allocates."""
+    least tfl_kv4_bytes bytes, whose contents are kept; work on it may be queued on the
+    current stream) or one that it allocates.  Outlives the calls on other streams than
+    the one it was made on."""
 
     def __init__(self, layers: int, n_kv: int, max_positions: int, buffer: torch.Tensor = None):
         nbytes = tfl_kv4_bytes(layers, n_kv, max_positions)
@@ -564,7 +566,8 @@ class KV4Rows:
 
 class KV4Attention:
     """tfl_kv4_attn and its workspace: attention of up to max_rows rows over caches
-    of up to max_positions positions."""
+    of up to max_positions positions.  Outlives the calls on other streams than the one
+    it was made on."""
 
     def __init__(self, n_q: int, n_kv: int, max_rows: int = 16, max_positions: int = 4096):
         nbytes = int(lib().tfl_kv4_attn_bytes(n_q, n_kv, 128, max_rows, max_positions))
