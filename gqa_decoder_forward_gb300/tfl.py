@@ -660,8 +660,10 @@ class KV4Runner:
         self.attention = KV4Attention(s.n_q, s.n_kv, max_rows, max_positions)
         self.step_ws = torch.empty(int(lib().tfl_kv4_step_workspace_bytes(model.handle)), dtype=torch.uint8,
                                    device="cuda")
-        self.prompt_ws = torch.empty(int(lib().tfl_kv4_prompt_workspace_bytes(model.handle, max_positions)),
-                                     dtype=torch.uint8, device="cuda")
+        # a model's prompts end at its max_context, whatever the caches hold
+        self.prompt_ws = torch.empty(
+            int(lib().tfl_kv4_prompt_workspace_bytes(model.handle, min(max_positions, model.cfg.max_context))),
+            dtype=torch.uint8, device="cuda")
 
     def kv(self, max_positions: int) -> KV4:
         return KV4(self.model.shape.layers, self.model.shape.n_kv, max_positions)

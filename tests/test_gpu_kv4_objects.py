@@ -109,3 +109,19 @@ def test_one_row_of_tensors_with_different_strides():
     tfl.tfl_kv4_write(tfl.KV4Rows([kv], [7], [1]), 0, k, wide[:, 1])
     tfl.tfl_kv4_write(tfl.KV4Rows([twin], [7], [1]), 0, k, v)
     assert torch.equal(kv.buffer, twin.buffer)
+
+
+def test_a_runner_for_longer_caches_than_the_models_context():
+    w = synth.model_weights(synth.TINY, 6, "cuda")
+    m = tfl.Model(synth.TINY, w, max_rows=64, max_decode_rows=4, max_context=200)
+    ids = synth.uniform_ids(7, 61, synth.TINY.vocab, "cuda")
+    out = [torch.empty((1, synth.TINY.vocab), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for lg, r in zip(out, (tfl.KV4Runner(m, max_rows=4), tfl.KV4Runner(m, max_rows=4, max_positions=200))):
+        kv = r.kv(1000)
+        r.prefill_chunk(kv, ids[:60].contiguous())
+        r.decode_step([kv], ids[60:].contiguous(), [1], lg)
+        kv.reset(150)
+        with pytest.raises(tfl.TflError) as e:                       # past the model's context
+            r.prefill_chunk(kv, ids[:60].contiguous())
+        assert e.value.code == tfl.TFL_E_CAPACITY
+    assert m.status() == tfl.TFL_OK and torch.equal(out[0].view(torch.int16), out[1].view(torch.int16))
