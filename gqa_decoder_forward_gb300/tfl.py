@@ -595,6 +595,8 @@ def _rows_arg(t: torch.Tensor, batch: KV4Rows, heads: int) -> int:
     if t.dtype is not torch.bfloat16 or not t.is_cuda or t.get_device() != batch.device:
         raise ValueError(f"expected a bf16 tensor on CUDA device {batch.device}")
     n = batch.total
+    if n == 0:
+        return heads * 128  # nothing is read or written: whatever the shape
     sh, st = t.shape, t.stride()
     if len(sh) == 2:
         ok = sh[1] == heads * 128 and st[1] == 1

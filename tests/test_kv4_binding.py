@@ -121,3 +121,13 @@ def test_one_row_may_be_a_tensor_of_one_row_beside_a_part_of_wider_rows():
         tfl.tfl_kv4_write(tfl.KV4Rows([cache_on(0)], [0], [1]), 0, one, wide, stream=0)
     with pytest.raises(ValueError):
         tfl.tfl_kv4_write(tfl.KV4Rows([cache_on(0)], [0], [2]), 0, rows_on(0), wide, stream=0)
+
+
+def test_a_call_without_rows_takes_an_empty_tensor_of_any_strides():
+    none = rows_on(0, rows=0)
+    none.stride = lambda: (0, 0, 0)
+    for call in (tfl.tfl_kv4_write, tfl.tfl_kv4_read):
+        with pytest.raises(tfl.TflError):                                # the library, of the NULL cache
+            call(tfl.KV4Rows([cache_on(0)], [0], [0]), 0, none, none, stream=0)
+        with pytest.raises(ValueError):
+            call(tfl.KV4Rows([cache_on(0)], [0], [1]), 0, none, none, stream=0)
