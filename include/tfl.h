@@ -545,6 +545,7 @@ int tfl_kv4_read(tfl_kv4* const* kvs, int n_streams, int layer, const int* pos0,
  * attend never matter, whatever their bytes.  Queries are to be below 2^115 in magnitude,
  * the sums over dims of |q| (|zero| + scale n) below 2^120, values below 2^115 / (keys
  * attended): beyond, fp16 operands or fp32 sums may overflow (to infinities or NaN).
+ * Numbers of a query 2^26 and more below its largest are rounded to 2^-34 of that one.
  * A row's result depends on its own query and its cache alone, bit for bit: not
  * on the other rows, streams or the capacity.
  *

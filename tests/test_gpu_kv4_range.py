@@ -81,3 +81,26 @@ def test_a_rows_bits_next_to_the_threshold_do_not_depend_on_its_neighbour():
     low, _ = ref.attention(q[0].astype(np.float64), 95, kq, (vq[0], vq[1], 0 * vq[2]))
     bound[:, 1::2] += 2.0 ** -20 * low[:, 0::2]
     assert (np.abs(alone[0] - out) <= bound).all()
+
+
+@pytest.mark.parametrize("rise,fall", [(12, 12), (12, 4), (9, 16), (20, 12), (12, -4), (-12, -4), (3, 12)])  # values to 2^90
+def test_scores_that_rise_while_the_values_scales_fall(rise, fall):
+    """Units of eleven steps (64 heads, of which two differ), each step's scores 2^rise above the one before (in the first row's
+    weights) and its values 2^fall below: the maximum moves again and again, and what came before counts, or not, or
+    counts alone."""
+    n, n_kv = 8600, 64                                  # 269 steps over 28 units at most: ten or more to a unit
+    steps = -(-(-(-n // 32)) // 28)
+    at = np.arange(n) // 32 % steps
+    r = np.random.default_rng(230)
+    k, v = 0.1 * r.normal(size=(n, 2, 128)), r.normal(size=(n, 2, 128))
+    k[:, 0, 0] = k[:, 1, 0] = rise * at                 # 0.1275 x 8 = 1.02 in the scores' log2
+    v *= 2.0 ** (50 - fall * at)[:, None, None]
+    k, v = bf16(k), bf16(v)
+    kv = cache_of(np.tile(k, (1, n_kv // 2, 1)), np.tile(v, (1, n_kv // 2, 1)))
+    q = queries(231, 1, n_kv, 0.3)
+    q[0, :, 0] = np.resize([8, 8, 4, -8, 0, 9], n_kv)
+    attn = tfl.KV4Attention(n_kv, n_kv, max_rows=1, max_positions=n)
+    got = attend(attn, [kv], [n - 1], [1], q)
+    kq, vq = ref.quantise(k), ref.quantise(v)
+    for h in range(0, 12, 2):                           # heads h and h + 1 hold the two that differ
+        check(got[:, h: h + 2], q[:, h: h + 2], [n - 1], kq, vq, f"heads {h}, {h + 1}")
