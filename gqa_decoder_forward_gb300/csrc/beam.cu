@@ -434,9 +434,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const bool largest = t >> 16 == m >> 16, usual = fabsf(z_max) < kHuge;
         const int E = usual ? exponent_of(z_max) : 0;
         if (t != 0u && usual) {
-            const int d = fabsf(z) < kHuge ? E - exponent_of(z) : 64;
+            const bool near = fabsf(z) < kHuge;  // (beyond, 64 and more below the row's largest: nothing, and not for exp_scaled)
+            const int d = near ? E - exponent_of(z) : 64;
             part = d < 60 ? sum >> (4 + d) : 0ull;
-            if (!largest) {
+            if (!largest && near) {
                 const float2 e = exp_scaled(z, E, pow);
                 part += (unsigned long long)count *
                         (unsigned long long)(__float2ll_rn(e.x * 35184372088832.f) + __float2ll_rn(e.y * 35184372088832.f));
