@@ -1699,14 +1699,21 @@ int tfl_beam_select(tfl_model* m, const void* logits, int n_groups, int beams, i
 
 int tfl_kv_reorder(tfl_model* m, tfl_kv* const* kvs, int n, const int* pos0, const int* rows, const int32_t* parents,
                    void* stream) {
+    return tfl_kv_reorder_rows(m, kvs, n, 0, pos0, rows, parents, stream);
+}
+
+int tfl_kv_reorder_rows(tfl_model* m, tfl_kv* const* kvs, int n, int first, const int* pos0, const int* rows,
+                        const int32_t* parents, void* stream) {
     if (!m || !kvs || !pos0 || !rows || !parents) return fail(TFL_E_ARG, "NULL model, kvs, pos0, rows or parents");
     if (n < 1 || n > kMaxStreams) return fail(TFL_E_ARG, "%d caches; a call takes 1..%d", n, kMaxStreams);
+    if (first < 0) return fail(TFL_E_ARG, "first %d < 0", first);
     if ((uintptr_t)parents & 3u) return fail(TFL_E_ARG, "misaligned parents");
     ReorderArgs a = {};
     a.n = n;
     a.n_kv = m->cfg.n_kv;
     a.layers = m->cfg.layers;
     a.parents = parents;
+    a.first = first;
     a.lo = 1 << 30;
     int cap = 1 << 30;
     for (int i = 0; i < n; ++i) {

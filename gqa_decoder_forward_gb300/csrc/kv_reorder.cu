@@ -1,7 +1,8 @@
 // Reordering of caches by parents: positions [begin[i], end[i]) of cache i become what
 // cache parents[i] held there, in every layer, keys and values.  The parents are in device
 // memory (a beam search's selection leaves them there), so which caches move is known to the
-// kernel alone; a parent outside 0..n-1, like a cache's own number, leaves the cache as it is.
+// kernel alone; a parent that is none of the call's caches (first .. first + n - 1), like a cache's own number, leaves the
+// cache as it is.
 //
 // In place, whatever the parents (two caches may change places): a thread holds the same
 // 16 bytes of every cache that has children and stores after it has loaded them all, and no
@@ -35,10 +36,11 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         int p = -1, page = 0, b = 0, e = 0;
         if (i < a.n) {
             p = a.parents[i];
+            p = p >= a.first && p - a.first < a.n ? p - a.first : -1;
             page = a.kv[i].table[pos / kPage];
             b = max(a.begin[i], pos) - pos;
             e = min(a.end[i], pos + run) - pos;
-            if (p == i || p < 0 || p >= a.n || b >= e) p = -1;  // stays
+            if (p == i || b >= e) p = -1;  // stays
         }
         const int parent_page = __shfl_sync(0xffffffffu, page, max(p, 0));
         const auto at = [&](const KvView& v, int page) {

@@ -10,6 +10,7 @@ struct ReorderArgs {
     int lo, hi;                // all ranges lie in [lo, hi)
     int run;                   // positions of a CTA, set by the launch
     const int* parents;        // device, n
+    int first;                 // the number that parents have for cache 0
     int begin[kMaxStreams], end[kMaxStreams];
     KvView kv[kMaxStreams];
 };

@@ -617,7 +617,9 @@ int tfl_prefill_chunk_kv4(tfl_model* model, tfl_kv4* kv, const int32_t* ids, int
  *   tfl_decode_step_shared (or tfl_decode_step, with whole caches) on the beams' ids,
  *   tfl_beam_select on its logits, whose ids and scores are the next step's,
  *   tfl_kv_reorder of the tails by its parents,
- * and needs no word from the host.
+ * and needs no word from the host.  A step and a reordering take up to 16 streams, a selection more rows: of searches
+ * with more beams in all, each step leaves its logits in rows of the selection's, and tfl_kv_reorder_rows moves 16
+ * caches at a time.
  */
 
 /*
@@ -629,7 +631,7 @@ int tfl_prefill_chunk_kv4(tfl_model* model, tfl_kv4* kv, const int32_t* ids, int
  * for the ids v of its n_out (1..32) largest logits (of equal ones the lower ids; none that is
  * -inf).  Per group the n_out best candidates, best first, scores compared as 64-bit numbers
  * (from sums good to 2^-28) and equal ones by the lower row, then the lower id: ids, parents (the
- * row r, as tfl_kv_reorder takes it) and out_scores (the score rounded to float), device
+ * row r of the call, as tfl_kv_reorder takes it up to 16 rows and tfl_kv_reorder_rows beyond) and out_scores (the score rounded to float), device
  * [n_groups][n_out] each.  Where a group has fewer candidates, the rest are id -1 (no token: a step
  * given it reports that), parent -1 (which moves no cache), score -inf (whose row offers nothing).
  *   done (device int32 [rows], NULL: none): a row with done[r] != 0 has ended and offers
@@ -658,6 +660,14 @@ int tfl_beam_select(tfl_model* model, const void* logits, int n_groups, int beam
  */
 int tfl_kv_reorder(tfl_model* model, tfl_kv* const* kvs, int n, const int* pos0, const int* rows,
                    const int32_t* parents, void* stream);
+
+/*
+ * The same for some of the rows that parents number: kvs[i] is the cache of row first + i (first >= 0), as of a group of
+ * a selection of more than 16 rows, whose parents are those of rows first .. first + n - 1.  A parent
+ * outside them leaves kvs[i] as it is.  tfl_kv_reorder is this with first = 0.
+ */
+int tfl_kv_reorder_rows(tfl_model* model, tfl_kv* const* kvs, int n, int first, const int* pos0, const int* rows,
+                        const int32_t* parents, void* stream);
 
 /*
  * Attention of one new token per stream over a prefix that a group of streams shares and a
