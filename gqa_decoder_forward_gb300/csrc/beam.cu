@@ -488,14 +488,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
         return;
     }
-    // The score of row b's logit of this order: added up in two fp32 numbers, as a 64-bit one in the end.
+    // The score of row b's logit of this order: added up in two fp32 numbers, as a 64-bit one in the end; in 64 bits from the start
+    // where it, or the logit's distance from the largest, is beyond fp32's range.
     const auto score_at = [&](int b, unsigned order) {
         float dh, dl, uh, ul, vh, vl;
         two_sum(logit_of(order), -row_top[b], dh, dl);
         two_sum(dh, -log_rest[b], uh, ul);
         two_sum(score[b], uh, vh, vl);
         const float rest = __fadd_rn(vl, __fadd_rn(__fadd_rn(dl, ul), -log_low[b]));
-        return order_of(isinf(vh) ? (double)vh : (double)vh + (double)rest);
+        if (isinf(vh)) {
+            const double d = (double)logit_of(order) - (double)row_top[b];
+            return order_of((double)score[b] + (d - ((double)log_rest[b] + (double)log_low[b])));
+        }
+        return order_of((double)vh + (double)rest);
     };
     // Who can be among the n best, in fp32 with a margin (double precision is slow for all): a candidate's score lies
     // within `off` of `near`; the n-th largest of some candidates' lower ends is a score that n candidates reach.

@@ -631,7 +631,8 @@ int tfl_prefill_chunk_kv4(tfl_model* model, tfl_kv4* kv, const int32_t* ids, int
  * for the ids v of its n_out (1..32) largest logits (of equal ones the lower ids; none that is
  * -inf).  Per group the n_out best candidates, best first, scores compared as 64-bit numbers
  * (from sums good to 2^-28) and equal ones by the lower row, then the lower id: ids, parents (the
- * row r of the call, as tfl_kv_reorder takes it up to 16 rows and tfl_kv_reorder_rows beyond) and out_scores (the score rounded to float), device
+ * row r of the call, as tfl_kv_reorder takes it up to 16 rows and tfl_kv_reorder_rows beyond) and out_scores (the score rounded to float: -inf
+ * below its lowest number, which ends what that row offers the next step), device
  * [n_groups][n_out] each.  Where a group has fewer candidates, the rest are id -1 (no token: a step
  * given it reports that), parent -1 (which moves no cache), score -inf (whose row offers nothing).
  *   done (device int32 [rows], NULL: none): a row with done[r] != 0 has ended and offers

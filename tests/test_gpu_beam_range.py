@@ -1,10 +1,13 @@
-"""tfl_beam_select where chunks of a row lie far below its largest logit: a vocabulary mask that adds a large negative
-number to a run of ids leaves the row's sum what it is without them.  The tolerance is test_gpu_beam_select's."""
+"""tfl_beam_select over fp32's whole range.  Chunks of a row far below its largest logit: a vocabulary mask that adds a large negative
+number to a run of ids leaves the row's sum what it is without them.  Scores below fp32's lowest number: compared in 64 bits
+all the same.  The tolerance is test_gpu_beam_select's."""
+import numpy as np
 import pytest
 import torch
 
-from gqa_decoder_forward_gb300 import build
-from tests.test_gpu_beam_select import BIG, check, normal, plain_model, scores_of
+from gqa_decoder_forward_gb300 import build, tfl
+from tests import beam_ref
+from tests.test_gpu_beam_select import BIG, TINY, check, normal, outputs, plain_model, scores_of
 
 pytestmark = pytest.mark.gpu
 CHUNK = 8192   # logits of a row that are summed together
@@ -46,3 +49,47 @@ def test_chunks_that_are_all_one_far_number(big, top):
     if top < 0:
         z -= 100.0
     check(big, z, scores_of(603, 16, 4), 32)
+
+
+@pytest.fixture(scope="module")
+def models(big):
+    return {"tiny": plain_model(TINY, 64), "33b": big}
+
+
+LOWEST = float(torch.finfo(torch.float32).min)
+
+
+def rows_beyond(kind, V):
+    """[4, V] logits, twelve ids of each row allowed, and [1, 4] scores: many candidates' scores are below fp32's lowest number."""
+    gen = torch.Generator().manual_seed(604)
+    z = torch.full((4, V), float("-inf"), dtype=torch.float64)
+    span = {"logits": 6.7e38, "scores": 3e38, "both": 6.7e38}[kind]       # from the largest down
+    scores = {"logits": [-3.0, -2.0, -5.0, -4.0], "scores": [-3.39e38, -3.395e38, LOWEST, -3.38e38],
+              "both": [-3.2e38, -1e38, -3.3e38, -2e38]}[kind]
+    for b in range(4):
+        allowed = torch.randperm(V, generator=gen)[:12]
+        z[b, allowed] = 3.35e38 - span * torch.rand(12, generator=gen).double()
+        z[b, allowed[0]] = 3.35e38
+    return z.to(torch.bfloat16), torch.tensor([scores], dtype=torch.float32)
+
+
+@pytest.mark.parametrize("n_out", [5, 32])
+@pytest.mark.parametrize("kind", ["logits", "scores", "both"])
+@pytest.mark.parametrize("name", ["tiny", "33b"])
+def test_scores_beyond_fp32(models, name, kind, n_out):
+    """Ranked by their 64-bit values all the same; out_scores is -inf where float32 is."""
+    m = models[name]
+    z, scores = rows_beyond(kind, m.shape.vocab)
+    ids, parents, ref, _ = beam_ref.select(z.double().numpy(), scores.double().numpy(), n_out)
+    with np.errstate(over="ignore"):
+        ref = ref.astype(np.float32)
+    assert np.isinf(ref).sum() > 1 or n_out < 32
+    assert len(set(parents[0].tolist())) > 1
+    out = outputs(1, n_out)
+    tfl.tfl_beam_select(m, z.cuda(), scores.cuda(), **out)
+    assert m.status() == tfl.TFL_OK
+    assert np.array_equal(out["parents"].cpu().numpy(), parents) and np.array_equal(out["ids"].cpu().numpy(), ids)
+    got = out["out_scores"].cpu().numpy()
+    assert np.array_equal(np.isinf(got), np.isinf(ref))
+    fine = np.isfinite(ref)
+    assert (np.abs(got[fine].astype(float) - ref[fine]) <= 2.0 ** -23 * np.abs(ref[fine].astype(float)) + 2.0 ** -28).all()
