@@ -17,8 +17,9 @@
 // table's 2^(j/32), held as two fp32 numbers, times a short series (P. T. P. Tang's table-driven method, ACM TOMS 15
 // (1989)), since double-precision arithmetic runs at 1/64 of the fp32 rate here.  A chunk's terms are good to 2^-29, what
 // the join computes from the sums to about 2^-40.  Sums are integers: a chunk's in units of 2^(E-49) with
-// E = ceil(z_max log2 e) of the chunk, a row's in units of 2^(E-45), so they do not depend on the order of addition.  The largest
-// logit is counted apart, so that a row in which nothing else counts has the score s_b itself.
+// E = ceil(z_max log2 e) of the chunk, a row's in units of 2^(E-45), so they do not depend on the order of addition; 16 logits are
+// added up in fp32 before, the same ones and in the same order in either size of CTA, so that a row's score does not depend on
+// the rest of the call.  The largest logit is counted apart, so that a row in which nothing else counts has the score s_b itself.
 //
 // Bound and measured (ids of 166,912, replayed from a graph).  64 rows of 16 beams, 32 kept (21.4 MB, 3.2 us of copying): 26.0
 // us, of which the chunks take 17: 38 instructions a logit, 15 of them the exponential's, in 64% of the issue slots; the
@@ -34,6 +35,7 @@ namespace beam {
 namespace {
 
 constexpr int kJoinThreads = 512;
+constexpr int kSumThreads = 512;         // sums of a chunk's exponentials, of the same 16 logits each however many threads there are
 constexpr int kReach = 2 * kMaxOut;      // threads of a chunk whose logits may reach its threshold
 constexpr unsigned kBad = 1u;            // flag: the chunk holds NaN or +Inf
 constexpr int kIdBits = 18;
@@ -137,6 +139,7 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__ Args a) {
     constexpr int kPer = kChunk / kThreads;  // logits of a thread, in 16-byte loads
     constexpr int kWarps = kThreads / 32;
+    constexpr int kSums = kSumThreads / kThreads;  // sums of a thread: over its eights s, s + kSums, ...
     static_assert(kReach * (kPer / 8) <= kThreads, "an eight of theirs to a thread");
     // The chunk: thread t's i-th eight logits at [i][t].  Passes over them are loops, not a copy of their body for each logit
     // (straight-line code that runs once is fetched slower than it runs); held here, since other threads look at
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__
     }
     pdl_wait();
     pdl_trigger();
-    const int at0 = chunk * kChunk, passes = (min(kChunk, a.V - at0) + kThreads * 8 - 1) / (kThreads * 8);
+    const int at0 = chunk * kChunk, passes = (min(kChunk, a.V - at0) + kSumThreads * 8 - 1) / (kSumThreads * 8) * kSums;
     uint4 w[kPer / 8];
 #pragma unroll
     for (int i = 0; i < kPer / 8; ++i) {
@@ -173,15 +176,21 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__
         pow_r[tid] = entry.y;
     }
     if (!row_live(a, row)) return;
-    unsigned m2 = 0xFF80FF80u;
+    bool bad = false;
+    unsigned best = 0u, bests[kSums];  // the largest of all a thread's logits, and of each of its sums'
 #pragma unroll
-    for (int i = 0; i < kPer / 8; ++i) {
-        m2 = max2_nan(max2_nan(m2, w[i].x), max2_nan(w[i].y, max2_nan(w[i].z, w[i].w)));
-        held[i][tid] = w[i];
+    for (int s = 0; s < kSums; ++s) {
+        unsigned m2 = 0xFF80FF80u;
+#pragma unroll
+        for (int i = s; i < kPer / 8; i += kSums) {
+            m2 = max2_nan(max2_nan(m2, w[i].x), max2_nan(w[i].y, max2_nan(w[i].z, w[i].w)));
+            held[i][tid] = w[i];
+        }
+        m2 = max2_nan(m2, __byte_perm(m2, m2, 0x1032)) & 0xFFFFu;
+        bad = bad || ((m2 & 0x7F80u) == 0x7F80u && m2 != 0xFF80u);  // a NaN, or +Inf
+        bests[s] = order_of(m2);
+        best = max(best, bests[s]);
     }
-    m2 = max2_nan(m2, __byte_perm(m2, m2, 0x1032)) & 0xFFFFu;
-    const bool bad = (m2 & 0x7F80u) == 0x7F80u && m2 != 0xFF80u;  // a NaN, or +Inf
-    const unsigned best = order_of(m2);
     const unsigned wm = __reduce_max_sync(0xffffffffu, best);
     __syncthreads();
     if (bad) bad_any = kBad;
@@ -265,18 +274,17 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__
     }
 
     // How often the largest occurs, and the sum of e^z over the others: e^z 2^-E = t 2^n (1 + r) 2^g with
-    // z log2 e = k/32 + g, as in exp_scaled but for (1 + r) 2^g - 1 in one fp32 number (good to 2^-29).  Per thread, with
-    // the E of its own largest, in two fp32 sums: multiples of 2^-18 (exact: at most 32) and what they leave, at most 2^-19 a
-    // term, so that what fp32 rounds is 2^-35 of the thread's largest in all, however many terms there are below it.
+    // z log2 e = k/32 + g, as in exp_scaled but for (1 + r) 2^g - 1 in one fp32 number (good to 2^-29).  Of 16 logits at a time, with
+    // the E of their own largest, in two fp32 sums: multiples of 2^-18 (exact: at most 16) and what they leave, at most 2^-19 a
+    // term, so that what fp32 rounds is 2^-35 of their largest in all, however many terms there are below it.
     // Then integers.
     const float z_max = logit_of(top);
     const bool huge = fabsf(z_max) >= kHuge;
-    const float z_own = fmaxf(best ? logit_of(best) : -INFINITY, z_max - 41.5f);
-    const float cut = z_own - 41.5f;  // e^-41.5 for each of the up to 2^18 logits below: 2^-41 in all
-    const int E = huge ? 0 : exponent_of(z_max), E_own = huge ? 0 : exponent_of(z_own);
-    const float round = kRound - (float)E_own;
+    const int E = huge ? 0 : exponent_of(z_max);
     unsigned count = 0u;
-    Pair whole = 0ull, rest = 0ull;
+    unsigned long long mine = 0ull;
+    float round;
+    Pair whole, rest;
     const auto add = [&](const float(&z)[8]) {
         Pair x[4], g[4], t[4], p[4];
 #pragma unroll
@@ -310,25 +318,35 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__
     const bool holds = __any_sync(0xffffffffu, best == top);
     if (!huge || holds) {
 #pragma unroll 1
-        for (int i = 0; i < passes; ++i) {
-            float z[8];
-            unpack(held[i][tid], z);
-            if (holds) {
+        for (int s = 0; s < kSums; ++s) {
+            const unsigned own = kSums > 1 && s > 0 ? bests[kSums - 1] : bests[0];
+            const float z_own = fmaxf(own ? logit_of(own) : -INFINITY, z_max - 41.5f);
+            const float cut = z_own - 41.5f;  // e^-41.5 for each of the up to 2^18 logits below: 2^-41 in all
+            const int E_own = huge ? 0 : exponent_of(z_own);
+            round = kRound - (float)E_own;
+            whole = rest = 0ull;
+#pragma unroll 1
+            for (int i = s; i < passes; i += kSums) {
+                float z[8];
+                unpack(held[i][tid], z);
+                if (holds) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    count += z[e] == z_max;
-                    z[e] = z[e] == z_max ? cut : z[e];
+                    for (int e = 0; e < 8; ++e) {
+                        count += z[e] == z_max;
+                        z[e] = z[e] == z_max ? cut : z[e];
+                    }
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = fmaxf(z[e], cut);
-            if (!huge) add(z);
+                for (int e = 0; e < 8; ++e) z[e] = fmaxf(z[e], cut);
+                if (!huge) add(z);
+            }
+            const float2 w2 = parts_of(whole), r2 = parts_of(rest);
+            const float wholes = __fadd_rn(w2.x, w2.y), rests = __fadd_rn(r2.x, r2.y);
+            if (!huge)
+                mine += (unsigned long long)((((long long)(wholes * 262144.f) << 31) + __float2ll_rn(rests * 562949953421312.f)) >>
+                                             (E - E_own));
         }
     }
-    const float2 w2 = parts_of(whole), r2 = parts_of(rest);
-    const float wholes = __fadd_rn(w2.x, w2.y), rests = __fadd_rn(r2.x, r2.y);
-    unsigned long long mine =
-        (unsigned long long)((((long long)(wholes * 262144.f) << 31) + __float2ll_rn(rests * 562949953421312.f)) >> (E - E_own));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     count = __reduce_add_sync(0xffffffffu, count);

@@ -634,7 +634,8 @@ int tfl_prefill_chunk_kv4(tfl_model* model, tfl_kv4* kv, const int32_t* ids, int
  * row r of the call, as tfl_kv_reorder takes it up to 16 rows and tfl_kv_reorder_rows beyond) and out_scores (the score rounded to float: -inf
  * below its lowest number, which ends what that row offers the next step), device
  * [n_groups][n_out] each.  Where a group has fewer candidates, the rest are id -1 (no token: a step
- * given it reports that), parent -1 (which moves no cache), score -inf (whose row offers nothing).
+ * given it reports that), parent -1 (which moves no cache), score -inf (whose row offers nothing).  What a group
+ * gives does not depend on the other groups of the call, bit for bit.
  *   done (device int32 [rows], NULL: none): a row with done[r] != 0 has ended and offers
  * (eos, scores[r]) alone; eos is then an id.  out_done (device int32 [n_groups][n_out], NULL:
  * none): 1 for a candidate whose row has ended or whose id is eos (-1: no id ends a row).
