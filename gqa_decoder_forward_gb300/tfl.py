@@ -803,8 +803,9 @@ def tfl_kv_reorder_rows(model: Model, batch: KVRows, first: int, parents: torch.
 
 class SharedRows:
     """Streams over shared prefixes: group g's streams[g] streams, each with a cache of tails, share prefixes[g] (None:
-    no prefix); n_prefix[g] positions of it (default: its length); stream s's row at position pos[s] (needed for
-    tfl_shared_attention alone).  Keeps the host arrays that the library takes (set: other positions)."""
+    no prefix); n_prefix[g] positions of it (default: its length now; a decode step takes whole prefixes, as long as they are
+    here); stream s's row at position pos[s] (needed for tfl_shared_attention alone).  Keeps the host arrays that the library
+    takes (set: other positions)."""
 
     def __init__(self, prefixes: Sequence[KV], streams: Sequence[int], tails: Sequence[KV], n_prefix: Sequence[int] = None,
                  pos: Sequence[int] = None):
@@ -873,8 +874,13 @@ def tfl_shared_wait_probe(runner: SharedRunner, batch: SharedRows, layer: int, q
 
 
 def tfl_decode_step_shared(runner: SharedRunner, batch: SharedRows, ids: torch.Tensor, logits: torch.Tensor, stream=None):
-    """tfl_decode_step of one id per stream, over shared prefixes; the caches' lengths say where the rows sit."""
+    """tfl_decode_step of one id per stream, over shared prefixes; the caches' lengths say where the rows sit, and the prefixes' have
+    to be the batch's, which its tails were made for."""
     m, n = runner.model, len(batch.tails)
+    for g, kv in enumerate(batch.prefixes):
+        length = 0 if kv is None else kv.length
+        if batch.n_prefix[g] != length:
+            raise ValueError(f"group {g}: a batch for {batch.n_prefix[g]} positions of a prefix whose length is {length}")
     if ids.dtype is not torch.int32 or ids.get_device() != _device_of(m) or ids.numel() != n or not ids.is_contiguous():
         raise ValueError(f"expected {n} contiguous int32 ids on CUDA device {_device_of(m)}, got {ids.dtype} "
                          f"{tuple(ids.shape)} strides {ids.stride()} on {ids.device}")

@@ -1,8 +1,9 @@
-"""Numbers that the binding of the beam operators hands to the library as C ints: refused where they do not fit, since ctypes
-would keep their low halves (no GPU)."""
+"""What the binding of the beam operators refuses because the library cannot see it: numbers that do not fit the C ints they
+become (ctypes would keep their low halves), and batches made for other lengths of their prefixes (no GPU)."""
 import pytest
+import torch
 
-from tests.test_beam_binding import cache, model, null_refused, t
+from tests.test_beam_binding import VOCAB, cache, model, null_refused, runner, t
 from gqa_decoder_forward_gb300 import build, tfl
 
 
@@ -19,3 +20,20 @@ def test_first_row_of_a_reordering():
     with pytest.raises(TypeError):
         tfl.tfl_kv_reorder_rows(model(), batch, 1.0, t(2), stream=0)
     null_refused(tfl.tfl_kv_reorder_rows, model(), batch, 16, t(2))
+
+
+def test_a_step_takes_the_prefixes_its_batch_was_made_for():
+    ids, logits = t(2), t(2, VOCAB, dtype=torch.bfloat16)
+    go = lambda batch: tfl.tfl_decode_step_shared(runner(), batch, ids, logits, stream=0)  # noqa: E731
+    for n_prefix in (6, 8, 0):                                   # positions that the step would not keep to
+        with pytest.raises(ValueError):
+            go(tfl.SharedRows([cache(7)], [2], [cache(), cache()], [n_prefix]))
+    with pytest.raises(ValueError):
+        go(tfl.SharedRows([None, cache(7)], [1, 1], [cache(), cache()], [0, 6]))
+    prefix = cache(7)
+    grown = tfl.SharedRows([prefix, None], [1, 1], [cache(), cache()])
+    null_refused(tfl.tfl_decode_step_shared, runner(), grown, ids, logits)
+    prefix.length = 8                                            # after the tails were made
+    with pytest.raises(ValueError):
+        go(grown)
+    null_refused(tfl.tfl_decode_step_shared, runner(), tfl.SharedRows([cache(7)], [2], [cache(), cache()], [7]), ids, logits)
