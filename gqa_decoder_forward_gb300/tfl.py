@@ -739,6 +739,13 @@ def _ints(values, n: int, what: str):
     return (ctypes.c_int * n)(*values)
 
 
+def _int32(x: int, what: str) -> int:
+    """x, which becomes a C int."""
+    if -2 ** 31 <= x < 2 ** 31:
+        return x
+    raise ValueError(f"{what} {x} outside 32 bits")
+
+
 def _device_of(model: Model) -> int:
     return model.workspace.get_device()
 
@@ -764,7 +771,8 @@ def tfl_beam_select(model: Model, logits: torch.Tensor, scores: torch.Tensor, id
     out, i32, f32 = (groups, n_out), torch.int32, torch.float32
     return _check(lib().tfl_beam_select(
         model.handle, _vector(logits, torch.bfloat16, (groups * beams, model.shape.vocab), dev, "logits"), groups, beams, n_out,
-        _vector(scores, f32, given, dev, "scores"), None if done is None else _vector(done, i32, given, dev, "done"), eos,
+        _vector(scores, f32, given, dev, "scores"), None if done is None else _vector(done, i32, given, dev, "done"),
+        _int32(eos, "eos"),
         _vector(ids, i32, out, dev, "ids"), _vector(parents, i32, out, dev, "parents"),
         _vector(out_scores, f32, out, dev, "out_scores"),
         None if out_done is None else _vector(out_done, i32, out, dev, "out_done"), _stream_of(logits, stream)))
@@ -797,7 +805,7 @@ def tfl_kv_reorder_rows(model: Model, batch: KVRows, first: int, parents: torch.
             or not parents.is_contiguous():
         raise ValueError(f"expected {batch.n} contiguous int32 parents on CUDA device {_device_of(model)}, got "
                          f"{parents.dtype} {tuple(parents.shape)} strides {parents.stride()} on {parents.device}")
-    return _check(lib().tfl_kv_reorder_rows(model.handle, batch.handles, batch.n, *_ints([first], 1, "first row"), batch.pos0,
+    return _check(lib().tfl_kv_reorder_rows(model.handle, batch.handles, batch.n, _int32(first, "first row"), batch.pos0,
                                             batch.rows, parents.data_ptr(), _stream_of(parents, stream)))
 
 
@@ -856,7 +864,7 @@ def _shared_args(runner: SharedRunner, batch: SharedRows, layer: int, q: torch.T
         raise ValueError("the batch has no positions")
     m, n, ws = runner.model, len(batch.tails), runner.workspace
     ldq, ldo = _head_rows(q, m, n, "q"), _head_rows(out, m, n, "out")
-    return (m.handle, layer, batch.prefix_handles, batch.n_prefix, batch.streams, batch.n_groups, batch.tail_handles, batch.pos,
+    return (m.handle, _int32(layer, "layer"), batch.prefix_handles, batch.n_prefix, batch.streams, batch.n_groups, batch.tail_handles, batch.pos,
             q.data_ptr(), ldq, out.data_ptr(), ldo, ws.data_ptr(), ws.numel())
 
 
@@ -869,8 +877,8 @@ def tfl_shared_wait_probe(runner: SharedRunner, batch: SharedRows, layer: int, q
                           spin_limit: int, stream=None):
     """tfl_shared_attention with a loader that stops at keys (2 k) or values (2 k + 1) of block k: tfl_status then reports
     TFL_E_DEVICE."""
-    return _check(lib().tfl_shared_wait_probe(*_shared_args(runner, batch, layer, q, out), lose, spin_limit,
-                                              _stream_of(q, stream)))
+    return _check(lib().tfl_shared_wait_probe(*_shared_args(runner, batch, layer, q, out), _int32(lose, "lose"),
+                                              _int32(spin_limit, "spin_limit"), _stream_of(q, stream)))
 
 
 def tfl_decode_step_shared(runner: SharedRunner, batch: SharedRows, ids: torch.Tensor, logits: torch.Tensor, stream=None):

@@ -3,7 +3,7 @@ become (ctypes would keep their low halves), and batches made for other lengths 
 import pytest
 import torch
 
-from tests.test_beam_binding import VOCAB, cache, model, null_refused, runner, t
+from tests.test_beam_binding import GOOD, HEADS, VOCAB, cache, model, null_refused, runner, t
 from gqa_decoder_forward_gb300 import build, tfl
 
 
@@ -17,8 +17,6 @@ def test_first_row_of_a_reordering():
     for first in (2 ** 32, 2 ** 31, -2 ** 31 - 1):
         with pytest.raises(ValueError):
             tfl.tfl_kv_reorder_rows(model(), batch, first, t(2), stream=0)
-    with pytest.raises(TypeError):
-        tfl.tfl_kv_reorder_rows(model(), batch, 1.0, t(2), stream=0)
     null_refused(tfl.tfl_kv_reorder_rows, model(), batch, 16, t(2))
 
 
@@ -37,3 +35,15 @@ def test_a_step_takes_the_prefixes_its_batch_was_made_for():
     with pytest.raises(ValueError):
         go(grown)
     null_refused(tfl.tfl_decode_step_shared, runner(), tfl.SharedRows([cache(7)], [2], [cache(), cache()], [7]), ids, logits)
+
+
+@pytest.mark.parametrize("big", [2 ** 32 + 2, 2 ** 31, -2 ** 31 - 1])
+def test_single_numbers(big):
+    with pytest.raises(ValueError):
+        tfl.tfl_beam_select(model(), **GOOD, eos=big, stream=0)
+    batch, q = tfl.SharedRows([cache(7)], [1], [cache()], pos=[7]), t(1, HEADS * 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        tfl.tfl_shared_attention(runner(), batch, big, q, q, stream=0)
+    for lose, limit in ((big, 1), (0, big)):
+        with pytest.raises(ValueError):
+            tfl.tfl_shared_wait_probe(runner(), batch, 0, q, q, lose, limit, stream=0)
