@@ -1342,6 +1342,10 @@ int tfl_kv_alloc(tfl_model* m, int max_positions, void* dev_buf, size_t bytes, t
     if (!aligned16(dev_buf)) return fail(TFL_E_ARG, "KV buffer not 16-byte aligned");
     const size_t need = tfl_kv_bytes(&m->cfg, max_positions);
     if (bytes < need) return fail(TFL_E_WORKSPACE, "KV buffer %zu bytes < %zu needed", bytes, need);
+    cudaPointerAttributes where;
+    CK(cudaPointerGetAttributes(&where, dev_buf));
+    if (where.type == cudaMemoryTypeDevice && where.device != m->device)
+        return fail(TFL_E_ARG, "the model is on device %d and the KV buffer on device %d", m->device, where.device);
     tfl_kv* kv = new tfl_kv();
     kv->model = m;
     kv->buf = (char*)dev_buf;

@@ -301,10 +301,13 @@ class KV:
     def __init__(self, model: Model, max_positions: int, buffer: torch.Tensor = None):
         self.model = model
         nbytes = tfl_kv_bytes(model.cfg, max_positions)
+        device = _device_of(model)
+        if device != torch.cuda.current_device():
+            raise ValueError(f"the model is on device {device} and the current device is {torch.cuda.current_device()}")
         if buffer is None:
             buffer = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        if not buffer.is_cuda or not buffer.is_contiguous() or buffer.get_device() != torch.cuda.current_device():
-            raise ValueError(f"expected a contiguous buffer on the current device, got strides {buffer.stride()} on {buffer.device}")
+        if not buffer.is_cuda or not buffer.is_contiguous() or buffer.get_device() != device:
+            raise ValueError(f"expected a contiguous buffer on the model's device, got strides {buffer.stride()} on {buffer.device}")
         self.buffer = buffer
         h = _vp()
         _settle()
@@ -840,7 +843,8 @@ class SharedRunner:
 
     def __init__(self, model: Model):
         self.model = model
-        self.workspace = torch.empty(int(lib().tfl_shared_workspace_bytes(model.handle)), dtype=torch.uint8, device="cuda")
+        self.workspace = torch.empty(int(lib().tfl_shared_workspace_bytes(model.handle)), dtype=torch.uint8,
+                                     device=model.workspace.device)
 
     def decode_step(self, batch: SharedRows, ids: torch.Tensor, logits: torch.Tensor, stream=None):
         return tfl_decode_step_shared(self, batch, ids, logits, stream)

@@ -150,7 +150,7 @@ const char* tfl_error_string(int code);
 size_t tfl_kv_bytes(const tfl_config* cfg, int max_positions);
 
 /*
- * Creates a KV object over dev_buf (16-byte aligned, >= tfl_kv_bytes bytes,
+ * Creates a KV object over dev_buf (memory of the model's device, 16-byte aligned, >= tfl_kv_bytes bytes,
  * owned by the caller).  1 <= max_positions <= cfg.max_context.  Writes the
  * identity page table (synchronously).  The length starts at 0.  The cache is
  * the position-major bf16 key/value cache of pull request #1415 ("How": prompt

@@ -1,10 +1,13 @@
 """What the binding of the beam operators refuses because the library cannot see it: numbers that do not fit the C ints they
-become (ctypes would keep their low halves), and batches made for other lengths of their prefixes (no GPU)."""
+become (ctypes would keep their low halves), batches made for other lengths of their prefixes, and caches on another device than
+their model's (no GPU: devices are stand-ins)."""
+import types
+
 import pytest
 import torch
 
 from tests.test_beam_binding import GOOD, HEADS, VOCAB, cache, model, null_refused, runner, t
-from gqa_decoder_forward_gb300 import build, tfl
+from gqa_decoder_forward_gb300 import build, synth, tfl
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -47,3 +50,17 @@ def test_single_numbers(big):
     for lose, limit in ((big, 1), (0, big)):
         with pytest.raises(ValueError):
             tfl.tfl_shared_wait_probe(runner(), batch, 0, q, q, lose, limit, stream=0)
+
+
+@pytest.mark.parametrize("model_on,current,buffer_on", [(0, 1, 1), (0, 1, 0), (0, 0, 1), (1, 0, 0), (0, 1, None)])
+def test_caches_are_made_on_their_models_device(monkeypatch, model_on, current, buffer_on):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    m = types.SimpleNamespace(handle=None, cfg=tfl.config(synth.TINY), workspace=types.SimpleNamespace(get_device=lambda: model_on))
+    buffer = None if buffer_on is None else types.SimpleNamespace(
+        is_cuda=True, is_contiguous=lambda: True, get_device=lambda: buffer_on, stride=lambda: (1,), device=f"cuda:{buffer_on}")
+    with pytest.raises(ValueError):
+        tfl.KV(m, 100, buffer=buffer)
+
+
+def test_a_runners_workspace_lies_on_its_models_device():
+    assert tfl.SharedRunner(model()).workspace.device == model().workspace.device
