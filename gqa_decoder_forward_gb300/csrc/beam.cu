@@ -21,11 +21,11 @@
 // added up in fp32 before, the same ones and in the same order in either size of CTA, so that a row's score does not depend on
 // the rest of the call.  The largest logit is counted apart, so that a row in which nothing else counts has the score s_b itself.
 //
-// Bound and measured (ids of 166,912, replayed from a graph).  64 rows of 16 beams, 32 kept (21.4 MB, 3.2 us of copying): 26.0
-// us, of which the chunks take 17: 38 instructions a logit, 15 of them the exponential's, in 64% of the issue slots; the
-// rest is a ninth CTA for some SMs that hold eight at a time, and phases of a CTA in which few warps work.  As long with five CTAs an SM;
-// with 19 chunks of 8,785 logits, so that all are there at once: 25.9.  The exponential as in the join: 34; one logit an
-// instruction: 26.4.  Four rows of one search: 8.6 us, the latency of two launches and of steps that wait for one
+// Bound and measured (ids of 166,912, replayed from a graph).  64 rows of 16 beams, 32 kept (21.4 MB, 3.2 us of copying): 25.9
+// us, of which the chunks take 17: 40 instructions a logit, 15 of them the exponential's, in 62% of the issue slots; the
+// rest is a second round of CTAs (1,344 chunks, six to an SM at a time), and phases of a CTA in which few warps work.  As long with
+// eight or five CTAs an SM; with 19 chunks of 8,785 logits, so that all are there at once: 25.9.  The exponential as in the join: 34; one
+// logit an instruction: 26.4.  Four rows of one search: 8.5 us, the latency of two launches and of steps that wait for one
 // another: loads, the largest, the n_out best and the sum, then the join's lists.
 #include "beam.cuh"
 #include "pair.cuh"
@@ -133,8 +133,8 @@ __device__ __forceinline__ unsigned max8(const uint4& c) {
     return max2_nan(m, __byte_perm(m, m, 0x1032)) & 0xFFFFu;
 }
 
-// With 256 threads the fewest instructions; with 512, where a CTA has an SM to itself, the shorter way (84 chunks: 8.6 and 8.3 us;
-// 1,344: 25.5 and 28.1).
+// With 256 threads the fewest instructions; with 512, where a CTA has an SM to itself, the shorter way (84 chunks: 8.75 and 8.5 us;
+// 21: 8.7 and 8.3; 1,344: 26.0 and 28.7).
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__ Args a) {
     constexpr int kPer = kChunk / kThreads;  // logits of a thread, in 16-byte loads

@@ -9,7 +9,7 @@
 // other thread touches those bytes.  What bounds it is the memory: a moved row is written once,
 // and read once however many children it has.
 // Measured (33B shape, all layers, replayed from a graph): 16 caches, 200 positions, 894.6 MB: 138 us, 6.5 TB/s, 96%
-// of a copy; 4 caches, 17 positions, 18.1 MB: 5.9 us, of which 2.7 are the memory's; two of the tiny model: 1.9 us, the launch.
+// of a copy; 4 caches, 17 positions, 18.1 MB: 6.2 us, of which 2.7 are the memory's; two of the tiny model: 2.0 us, the launch.
 #include "kv_reorder.cuh"
 
 namespace tfl {

@@ -26,12 +26,12 @@
 // one product of 128 rows does for both, with the same bits as two (8 beams after 131,072 keys: 85 us, 98 with two products;
 // 16 streams on four prompts of 300 to 31,999: 49.5 and 59.8; measured before the last steps).
 //
-// Bound and measured (33B heads: 56 on 8, one layer, replayed from a graph).  Eight beams after 131,072 keys: 84 us, 539 MB at
-// 6.4 TB/s, 94% of a copy; the memory bounds it (a block's products take 1,800 cycles of the 2,950 that it takes to come).
+// Bound and measured (33B heads: 56 on 8, one layer, replayed from a graph).  Eight beams after 131,072 keys: 83.5 us, 539 MB at
+// 6.5 TB/s, 95% of a copy; the memory bounds it (a block's products take 1,800 cycles of the 2,950 that it takes to come).
 // 16 beams after as many: 99 us; 112 rows' weights, which one warp per scheduler makes, take a little longer than their block.
 // 16 beams 100 tokens after 8,192 keys: 20.3 us for 40.6 MB (6.0 us): three to four blocks per SM, of which the
 // first comes after 4 us of launch, queries and page table, and the last weights, products, partials (8 MB, written and read) and
-// the join follow one another.  Four beams 17 tokens after 1,000: 8.6 us, latency alone.
+// the join follow one another.  Four beams 17 tokens after 1,000: 8.5 us, latency alone.
 //   Tried: a CTA per unit with two halves of a row in two warpgroups (33 us for the 16 beams), units shared out evenly by their
 // blocks over all caches (no gain, and a row's bits would depend on the others), several tails in one product (another
 // stream's values times a weight of 0 are NaN where they are not finite).
