@@ -796,20 +796,25 @@ class KVRows:
         self.pos0, self.rows = pos0, rows
 
 
+def _parents(model: Model, batch: KVRows, parents: torch.Tensor) -> int:
+    if parents.dtype is not torch.int32 or parents.get_device() != _device_of(model) or parents.numel() != batch.n \
+            or not parents.is_contiguous():
+        raise ValueError(f"expected {batch.n} contiguous int32 parents on CUDA device {_device_of(model)}, got "
+                         f"{parents.dtype} {tuple(parents.shape)} strides {parents.stride()} on {parents.device}")
+    return parents.data_ptr()
+
+
 def tfl_kv_reorder(model: Model, batch: KVRows, parents: torch.Tensor, stream=None):
     """The ranges of batch take what the caches numbered by parents (int32, one per cache) hold there."""
-    return tfl_kv_reorder_rows(model, batch, 0, parents, stream)
+    return _check(lib().tfl_kv_reorder(model.handle, batch.handles, batch.n, batch.pos0, batch.rows,
+                                       _parents(model, batch, parents), _stream_of(parents, stream)))
 
 
 def tfl_kv_reorder_rows(model: Model, batch: KVRows, first: int, parents: torch.Tensor, stream=None):
     """tfl_kv_reorder where batch's caches are those of rows first .. first + n - 1 of a larger call, which parents number
     (the group's row of a selection's parents)."""
-    if parents.dtype is not torch.int32 or parents.get_device() != _device_of(model) or parents.numel() != batch.n \
-            or not parents.is_contiguous():
-        raise ValueError(f"expected {batch.n} contiguous int32 parents on CUDA device {_device_of(model)}, got "
-                         f"{parents.dtype} {tuple(parents.shape)} strides {parents.stride()} on {parents.device}")
     return _check(lib().tfl_kv_reorder_rows(model.handle, batch.handles, batch.n, _int32(first, "first row"), batch.pos0,
-                                            batch.rows, parents.data_ptr(), _stream_of(parents, stream)))
+                                            batch.rows, _parents(model, batch, parents), _stream_of(parents, stream)))
 
 
 class SharedRows:
